@@ -52,29 +52,29 @@ def _update(name, encoders, width, rank, embedding):
 def listed():
     return [
         # one token through a block of the served encoder-sized model: all launch latency
-        _norm("norm, one token", 1, 768, "bf16", "bf16", True, False),
+        _norm("norm one token", 1, 768, "bf16", "bf16", True, False),
         # the norm after a sublayer of the six-encoder model at its training batch of 128 x 128
-        _norm("norm, 768 bf16 training", 16384, 768, "bf16", "bf16", True, True),
+        _norm("norm 768 bf16 training", 16384, 768, "bf16", "bf16", True, True),
         # an fp32 residual stream into the e4m3 layers of the 1024-wide model
-        _norm("norm, 1024 f32 to e4m3", 16384, 1024, "f32", "fp8", True, True),
+        _norm("norm 1024 f32 to e4m3", 16384, 1024, "f32", "fp8", True, True),
         # rows of no aligned length, a token count that no tile divides, no residual
-        _norm("norm, odd rows f32", 4093, 1001, "f32", "f32", False, True),
+        _norm("norm odd rows f32", 4093, 1001, "f32", "f32", False, True),
         # the six-encoder model's batch: 128 sequences of 128, the first ([CLS]) token kept visible
-        _attention("attention, 128 x 128", 128, 128, 12, 12, 64, 32, 32, 1, "bf16", False, True),
+        _attention("attention 128 x 128", 128, 128, 12, 12, 64, 32, 32, 1, "bf16", False, True),
         # pre-training on long documents at the 1024-wide model's heads
-        _attention("attention, 2 x 8192", 2, 8192, 16, 16, 64, 512, 512, 4, "bf16", False, True),
+        _attention("attention 2 x 8192", 2, 8192, 16, 16, 64, 512, 512, 4, "bf16", False, True),
         # packed prompts of a served decoder with shared key heads, lengths from 1 up
-        _attention("attention, ragged prompts", 24, 2048, 16, 4, 128, 511, 0, 4, "bf16", True, False),
+        _attention("attention ragged prompts", 24, 2048, 16, 4, 128, 511, 0, 4, "bf16", True, False),
         # the fp32 workload's batch, sequences of unequal length packed without padding
-        _attention("attention, ragged f32", 32, 128, 12, 12, 64, 64, 64, 1, "f32", True, True),
+        _attention("attention ragged f32", 32, 128, 12, 12, 64, 64, 64, 1, "f32", True, True),
         # one new token for each of 64 conversations over their caches
-        _decode("decode, 64 x 8192", 64, 8192, 16, 16, 64, 1023, 4, "bf16"),
+        _decode("decode 64 x 8192", 64, 8192, 16, 16, 64, 1023, 4, "bf16"),
         # one conversation: latency
-        _decode("decode, 1 x 1000", 1, 1000, 12, 4, 64, -1, 0, "bf16"),
+        _decode("decode 1 x 1000", 1, 1000, 12, 4, 64, -1, 0, "bf16"),
         # the cores of one encoder of the six-encoder model and of its embedding table
-        _update("update, one encoder", 1, 768, 30, True),
+        _update("update one encoder", 1, 768, 30, True),
         # every core of the 24-encoder model at rank 64
-        _update("update, 24 encoders", 24, 1024, 64, False),
+        _update("update 24 encoders", 24, 1024, 64, False),
     ]
 
 
