@@ -1,8 +1,9 @@
-"""Python binding of libttc (the C ABI declared in include/ttc.h).
+"""Python binding of libttc (the C ABI declared in include/ttc.h and
+include/ttc_block.h).
 
-Argument marshalling only: every step of the TT-linear and TTM-embedding
-computations runs in the HIP kernels of libttc.so.  PyTorch supplies device
-memory and the current stream.  Importing this module does not need a GPU;
+Argument marshalling only: every step of the computations runs in the HIP
+kernels of libttc.so.  PyTorch supplies device memory and the current stream.
+Importing this module does not need a GPU;
 loading the library does need the built ``libttc.so`` (``python -m
 tensor_train_compressed_tt_amd.build``) and fails loudly without it.
 """
@@ -33,7 +34,7 @@ STATUS = {
     8: "TTC_ERR_HIP",
 }
 
-# every symbol include/ttc.h declares
+# every symbol the headers in include/ declare
 EXPORTS = [
     "tt_linear_workspace",
     "tt_linear_fwd",
@@ -63,6 +64,9 @@ EXPORTS = [
     "ttc_trace_stop",
     "ttc_trace_count",
     "ttc_trace_get",
+    "ttc_norm_workspace",
+    "ttc_norm_fwd",
+    "ttc_norm_bwd",
 ]
 
 
@@ -105,6 +109,15 @@ class TTMEmbedDesc(ctypes.Structure):
 TTC_TTM_DEDUP, TTC_TTM_UNIQUE, TTC_TTM_PLAIN = 0, 1, 2
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -121,6 +134,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     D = ctypes.POINTER(TTLinearDesc)
     E = ctypes.POINTER(TTMEmbedDesc)
+    N = ctypes.POINTER(NormDesc)
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "tt_linear_workspace": [D, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
@@ -152,6 +166,9 @@ def lib() -> ctypes.CDLL:
         "ttm_embed_index": [E, _I64, _P, _P, _SZ, _P],
         "ttm_embed_lookup": [E, _I64, pp, pp, _P, _P, _SZ, _P, _SZ, _P],
         "ttm_embed_bwd": [E, _I64, _P, _P, pp, pp, _P, _SZ, pp, _P, _SZ, _P],
+        "ttc_norm_workspace": [N, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+        "ttc_norm_fwd": [N, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+        "ttc_norm_bwd": [N, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _SZ, _P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -427,6 +444,27 @@ def ttm_embed_bwd(desc, T, ids, dout, F, D, saved, saved_bytes, dF, scratch, scr
     _check("ttm_embed_bwd", code)
 
 
+def make_norm_desc(n, x_dtype=TTC_F32, y_dtype=TTC_F32, eps=1e-5):
+    return NormDesc(int(n), int(x_dtype), int(y_dtype), float(eps))
+
+
+def ttc_norm_workspace(desc: NormDesc, T: int):
+    s, c = _SZ(0), _SZ(0)
+    _check("ttc_norm_workspace", lib().ttc_norm_workspace(ctypes.byref(desc), T, ctypes.byref(s), ctypes.byref(c)))
+    return s.value, c.value
+
+
+def ttc_norm_fwd(desc, T, x, res, gamma, beta, h, y, saved, saved_bytes, stream=0):
+    code = lib().ttc_norm_fwd(ctypes.byref(desc), T, x, res, gamma, beta, h, y, saved, saved_bytes, stream)
+    _check("ttc_norm_fwd", code)
+
+
+def ttc_norm_bwd(desc, T, dy, h, gamma, dh, saved, saved_bytes, dx, dgamma, dbeta, scratch, scratch_bytes, stream=0):
+    code = lib().ttc_norm_bwd(ctypes.byref(desc), T, dy, h, gamma, dh, saved, saved_bytes, dx, dgamma, dbeta, scratch,
+                              scratch_bytes, stream)
+    _check("ttc_norm_bwd", code)
+
+
 def trace_start():
     _check("ttc_trace_start", lib().ttc_trace_start())
 
@@ -461,3 +499,4 @@ from .torch_api import (  # noqa: E402,F401
     rank_grads_batch,
     prepare_batch,
 )
+from .block_api import LayerNorm  # noqa: E402,F401

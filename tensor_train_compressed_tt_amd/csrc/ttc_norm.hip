@@ -1,0 +1,604 @@
+// Layer norm with the residual sum, forward and backward, for gfx950.
+//
+// Forward, per row of n elements: h = x + r, mean = sum h / n, var =
+// sum (h - mean)^2 / n, y = (h - mean) / sqrt(var + eps) * gamma + beta.
+// Backward, with xhat = (h - mean) rstd and u = dy gamma:
+//   dx = (u - mean(u) - xhat mean(u xhat)) rstd + dh,
+//   dgamma = sum_t dy xhat,  dbeta = sum_t dy.
+// Both passes are bound by memory: the forward reads x and r and writes h and
+// y, the backward reads dy, h and dh and writes dx, each once.  A row of up to
+// 4096 elements therefore stays in registers between its sums and its output
+// (one wave per row up to 1024 elements, four above), sums are fp32, and the
+// variance is summed from the centred values (a second sum over registers
+// costs no traffic and does not cancel).  Longer rows are read again from the
+// caches.  Weight gradients: a wave keeps its columns' sums over all its rows
+// in registers, a work-group adds its waves' in LDS, and a second launch adds
+// the work-groups' partials, always in the same order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/ttc_block.h"
+#include "ttc_device.hpp"
+#include "ttc_trace.hpp"
+
+namespace ttc {
+namespace {
+
+constexpr int kFwdThreads = 256;
+// The backward runs one work-group of 16 waves per CU: four waves per SIMD
+// keep enough rows in flight, and the fewer the work-groups, the fewer the
+// partial sums of the weight gradients.
+constexpr int kBwdThreads = 1024;
+constexpr int kBwdGroups = 256;
+constexpr int kFwdGroups = 2048;  // eight work-groups of four waves per CU
+constexpr int kRegN = 4096;       // longest row held in registers
+constexpr int kLongThreads = 1024;
+constexpr int kLongCols = 256;  // columns of a weight-gradient work-group of long rows
+constexpr float kFp8Max = 448.f;
+
+struct NormArgs {
+  const void* x;
+  const void* res;
+  const void* dy;
+  const void* dh;
+  const float* gamma;
+  const float* beta;
+  void* h;    // forward: written; backward: read
+  void* y;    // forward: y; backward: dx
+  float2* stats;
+  float* part;  // backward: partial sums, [work-group][2n]
+  int64_t T;
+  int n;
+  float eps;
+};
+
+// One row as a buffer resource: a load past its end gives zeros and a store
+// there is dropped, so the last lanes need no branch, and an element's address
+// is one 32-bit offset.  The row number must be the same in the whole wave.
+template <typename T>
+__device__ __forceinline__ rsrc_t row_rsrc(const void* base, int row, int n) {
+  typedef typename Elem<T>::type E;
+  return make_rsrc(static_cast<const E*>(base) + (int64_t)row * n, (int64_t)n * (int64_t)sizeof(E));
+}
+
+// VE = 4 needs rows of a multiple of four elements
+template <typename T, int VE>
+__device__ __forceinline__ void load_vec(rsrc_t r, int c, float (&v)[VE]) {
+  typedef typename Elem<T>::type E;
+  const int off = c * (int)sizeof(E);
+  if constexpr (VE == 1) {
+    if constexpr (sizeof(E) == 4)
+      v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    else if constexpr (sizeof(E) == 2)
+      v[0] = elem_to_f32<T>((E)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+    else
+      v[0] = elem_to_f32<T>((E)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0));
+  } else {
+    typedef E vec __attribute__((ext_vector_type(VE)));
+    vec q;
+    if constexpr (sizeof(E) == 4)
+      q = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    else if constexpr (sizeof(E) == 2)
+      q = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    else
+      q = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+#pragma unroll
+    for (int e = 0; e < VE; ++e) v[e] = elem_to_f32<T>(q[e]);
+  }
+}
+
+// nearest even; e4m3 saturates (a comparison with NaN is false, so NaN stays)
+template <typename T>
+__device__ __forceinline__ typename Elem<T>::type round_elem(float f) {
+  if constexpr (sizeof(typename Elem<T>::type) == 1) f = fabsf(f) > kFp8Max ? copysignf(kFp8Max, f) : f;
+  return Mma<T>::from_f32(f);
+}
+
+template <typename T, int VE>
+__device__ __forceinline__ void store_vec(rsrc_t r, int c, const float (&v)[VE]) {
+  typedef typename Elem<T>::type E;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(E);
+  if constexpr (VE == 1) {
+    buf_store(r, off, round_elem<T>(v[0]));
+  } else {
+    typedef E vec __attribute__((ext_vector_type(VE)));
+    vec q;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) q[e] = round_elem<T>(v[e]);
+    if constexpr (sizeof(E) == 4)
+      buf_store_f32x4(r, off, __builtin_bit_cast(f32x4, q));
+    else if constexpr (sizeof(E) == 2)
+      buf_store8(r, off, __builtin_bit_cast(uint2, q));
+    else
+      buf_store32(r, off, __builtin_bit_cast(unsigned, q));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float rounded(float f) {
+  return elem_to_f32<T>(Mma<T>::from_f32(f));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// Sum over the WPR waves of a row; `slot`: WPR floats of LDS of this row.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* slot, int wave) {
+  v = wave_sum(v);
+  if constexpr (WPR > 1) {
+    __syncthreads();  // the slots' last readers are done
+    if ((threadIdx.x & 63) == 0) slot[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) v += slot[w];
+  }
+  return v;
+}
+
+// A row in registers: element (j * 64 * WPR + lane) * VE + e is v[j][e]; those
+// past the row's end hold zeros.
+template <typename TX, typename TY, int VE, int WPR, int NV>
+__global__ __launch_bounds__(kFwdThreads) void k_norm_fwd(NormArgs a) {
+  constexpr int L = 64 * WPR, RPG = kFwdThreads / L;
+  __shared__ float slots[RPG * WPR];
+  const int li = threadIdx.x % L, wave = li / 64, n = a.n, T = (int)a.T;
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / L);
+  const rsrc_t rg = row_rsrc<float>(a.gamma, 0, n), rb = row_rsrc<float>(a.beta, 0, n);
+  float g[NV][VE], b[NV][VE];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    load_vec<float, VE>(rg, (j * L + li) * VE, g[j]);
+    load_vec<float, VE>(rb, (j * L + li) * VE, b[j]);
+  }
+  // with several waves to a row (RPG = 1) every thread of a work-group makes
+  // the same number of turns, as the barriers inside need
+  for (int64_t t64 = (int64_t)blockIdx.x * RPG + sub; t64 < T; t64 += (int64_t)gridDim.x * RPG) {
+    const int t = (int)t64;
+    float v[NV][VE];
+    const rsrc_t rx = row_rsrc<TX>(a.x, t, n);
+    if (a.res) {
+      const rsrc_t rr = row_rsrc<TX>(a.res, t, n), rh = row_rsrc<TX>(a.h, t, n);
+      float r[NV][VE];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        load_vec<TX, VE>(rx, (j * L + li) * VE, v[j]);
+        load_vec<TX, VE>(rr, (j * L + li) * VE, r[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[j][e] = rounded<TX>(v[j][e] + r[j][e]);
+        store_vec<TX, VE>(rh, (j * L + li) * VE, v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_vec<TX, VE>(rx, (j * L + li) * VE, v[j]);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s += v[j][e];
+    const float mean = row_sum<WPR>(s, slots + sub * WPR, wave) / n;
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (j * L + li) * VE < n;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        v[j][e] = in ? v[j][e] - mean : 0.f;
+        q += v[j][e] * v[j][e];
+      }
+    }
+    const float var = row_sum<WPR>(q, slots + sub * WPR, wave) / n;
+    const float rstd = 1.f / sqrtf(var + a.eps);
+    if (li == 0) a.stats[t] = make_float2(mean, rstd);
+    const rsrc_t ry = row_rsrc<TY>(a.y, t, n);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) v[j][e] = v[j][e] * rstd * g[j][e] + b[j][e];
+      store_vec<TY, VE>(ry, (j * L + li) * VE, v[j]);
+    }
+  }
+}
+
+template <typename TX, typename TY, int VE, int WPR, int NV>
+__global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(NormArgs a) {
+  constexpr int L = 64 * WPR, RPG = kBwdThreads / L;
+  extern __shared__ float lds[];  // RPG rows of n sums
+  __shared__ float slots[RPG * WPR];
+  const int li = threadIdx.x % L, wave = li / 64, n = a.n, T = (int)a.T;
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / L);
+  const rsrc_t rg = row_rsrc<float>(a.gamma, 0, n);
+  float g[NV][VE], dg[NV][VE], db[NV][VE];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    load_vec<float, VE>(rg, (j * L + li) * VE, g[j]);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) dg[j][e] = db[j][e] = 0.f;
+  }
+  const float inv_n = 1.f / n;
+  // every thread makes the work-group's number of turns (the barriers inside
+  // row_sum); past the last row, the resources are empty: zeros are read and
+  // nothing is written
+  for (int64_t t0 = (int64_t)blockIdx.x * RPG; t0 < T; t0 += (int64_t)gridDim.x * RPG) {
+    const bool row = t0 + sub < T;
+    const int t = row ? (int)(t0 + sub) : 0, len = row ? n : 0;
+    const float2 st = a.stats[t];
+    const rsrc_t ru = make_rsrc(static_cast<const typename Elem<TY>::type*>(a.dy) + (int64_t)t * n,
+                                len * (int64_t)sizeof(typename Elem<TY>::type));
+    typedef typename Elem<TX>::type EX;
+    const int64_t bytes = len * (int64_t)sizeof(EX);
+    const rsrc_t rx = make_rsrc(static_cast<const EX*>(a.h) + (int64_t)t * n, bytes);
+    const rsrc_t rd = make_rsrc(static_cast<const EX*>(a.dh) + (a.dh ? (int64_t)t * n : 0), a.dh ? bytes : 0);
+    float u[NV][VE], xh[NV][VE], d[NV][VE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      load_vec<TY, VE>(ru, (j * L + li) * VE, u[j]);
+      load_vec<TX, VE>(rx, (j * L + li) * VE, xh[j]);
+      load_vec<TX, VE>(rd, (j * L + li) * VE, d[j]);
+    }
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (j * L + li) * VE < len;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        xh[j][e] = in ? (xh[j][e] - st.x) * st.y : 0.f;
+        dg[j][e] += u[j][e] * xh[j][e];
+        db[j][e] += u[j][e];
+        u[j][e] *= g[j][e];
+        s1 += u[j][e];
+        s2 += u[j][e] * xh[j][e];
+      }
+    }
+    const float c1 = row_sum<WPR>(s1, slots + sub * WPR, wave) * inv_n;
+    const float c2 = row_sum<WPR>(s2, slots + sub * WPR, wave) * inv_n;
+    const rsrc_t ry = make_rsrc(static_cast<const EX*>(a.y) + (int64_t)t * n, bytes);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) u[j][e] = (u[j][e] - c1 - xh[j][e] * c2) * st.y + d[j][e];
+      store_vec<TX, VE>(ry, (j * L + li) * VE, u[j]);
+    }
+  }
+  // the work-group's sums: its rows' in order, dgamma first, then dbeta
+  float* out = a.part + (int64_t)blockIdx.x * 2 * n;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * L + li) * VE;
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (c < n) lds[sub * n + c + e] = k == 0 ? dg[j][e] : db[j][e];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += kBwdThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < RPG; ++r) s += lds[r * n + c];
+      out[k * n + c] = s;
+    }
+  }
+}
+
+// Adds P partials per column; a work-group takes 64 of the 2n columns, a wave
+// every 16th partial, and the waves' sums are added in wave order.
+__global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ part, int P, int n,
+                                                      float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  __shared__ float sum[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane, n2 = 2 * (int64_t)n;
+  float s = 0.f;
+  if (c < n2) {
+#pragma unroll 8
+    for (int p = w; p < P; p += 16) s += part[p * n2 + c];
+  }
+  sum[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < n2) {
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += sum[k][lane];
+    if (c < n)
+      dgamma[c] = s;
+    else
+      dbeta[c - n] = s;
+  }
+}
+
+// ---- rows over kRegN elements: a work-group per row, read again per step ----
+
+__device__ __forceinline__ float group_sum(float v, float* slots) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kLongThreads / 64; ++w) v += slots[w];
+  return v;
+}
+
+template <typename TX, typename TY>
+__global__ __launch_bounds__(kLongThreads) void k_norm_fwd_long(NormArgs a) {
+  __shared__ float slots[kLongThreads / 64];
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const rsrc_t rx = row_rsrc<TX>(a.x, (int)t, a.n), ry = row_rsrc<TY>(a.y, (int)t, a.n);
+    const rsrc_t rr = row_rsrc<TX>(a.res ? a.res : a.x, (int)t, a.n);
+    float v[1], r[1], s = 0.f, q = 0.f;
+    // a thread reads back in later steps only what it wrote itself
+    const rsrc_t src = row_rsrc<TX>(a.res ? a.h : a.x, (int)t, a.n);
+    for (int c = threadIdx.x; c < a.n; c += kLongThreads) {
+      load_vec<TX, 1>(rx, c, v);
+      if (a.res) {
+        load_vec<TX, 1>(rr, c, r);
+        v[0] = rounded<TX>(v[0] + r[0]);
+        store_vec<TX, 1>(src, c, v);
+      }
+      s += v[0];
+    }
+    const float mean = group_sum(s, slots) / a.n;
+    for (int c = threadIdx.x; c < a.n; c += kLongThreads) {
+      load_vec<TX, 1>(src, c, v);
+      q += (v[0] - mean) * (v[0] - mean);
+    }
+    const float rstd = 1.f / sqrtf(group_sum(q, slots) / a.n + a.eps);
+    if (threadIdx.x == 0) a.stats[t] = make_float2(mean, rstd);
+    for (int c = threadIdx.x; c < a.n; c += kLongThreads) {
+      load_vec<TX, 1>(src, c, v);
+      v[0] = (v[0] - mean) * rstd * a.gamma[c] + a.beta[c];
+      store_vec<TY, 1>(ry, c, v);
+    }
+  }
+}
+
+template <typename TX, typename TY>
+__global__ __launch_bounds__(kLongThreads) void k_norm_dx_long(NormArgs a) {
+  __shared__ float slots[kLongThreads / 64];
+  const float inv_n = 1.f / a.n;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const rsrc_t ru = row_rsrc<TY>(a.dy, (int)t, a.n), rx = row_rsrc<TX>(a.h, (int)t, a.n);
+    const rsrc_t rd = row_rsrc<TX>(a.dh ? a.dh : a.h, (int)t, a.n), ry = row_rsrc<TX>(a.y, (int)t, a.n);
+    const float2 st = a.stats[t];
+    float u[1], x[1], d[1] = {0.f}, s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.n; c += kLongThreads) {
+      load_vec<TY, 1>(ru, c, u);
+      load_vec<TX, 1>(rx, c, x);
+      u[0] *= a.gamma[c];
+      s1 += u[0];
+      s2 += u[0] * (x[0] - st.x) * st.y;
+    }
+    const float c1 = group_sum(s1, slots) * inv_n;
+    const float c2 = group_sum(s2, slots) * inv_n;
+    for (int c = threadIdx.x; c < a.n; c += kLongThreads) {
+      load_vec<TY, 1>(ru, c, u);
+      load_vec<TX, 1>(rx, c, x);
+      if (a.dh) load_vec<TX, 1>(rd, c, d);
+      u[0] = (u[0] * a.gamma[c] - c1 - (x[0] - st.x) * st.y * c2) * st.y + d[0];
+      store_vec<TX, 1>(ry, c, u);
+    }
+  }
+}
+
+// Weight-gradient partials of long rows: work-group (x, y) sums kLongCols
+// columns over the y-th of gridDim.y ranges of rows, in row order.
+template <typename TX, typename TY>
+__global__ __launch_bounds__(kLongCols) void k_norm_dw_long(NormArgs a) {
+  const int c = blockIdx.x * kLongCols + threadIdx.x;
+  if (c >= a.n) return;
+  const int64_t t0 = a.T * blockIdx.y / gridDim.y, t1 = a.T * (blockIdx.y + 1) / gridDim.y;
+  float u[1], x[1], sg = 0.f, sb = 0.f;
+  for (int64_t t = t0; t < t1; ++t) {
+    const float2 st = a.stats[t];
+    load_vec<TY, 1>(row_rsrc<TY>(a.dy, (int)t, a.n), c, u);
+    load_vec<TX, 1>(row_rsrc<TX>(a.h, (int)t, a.n), c, x);
+    sg += u[0] * (x[0] - st.x) * st.y;
+    sb += u[0];
+  }
+  float* out = a.part + (int64_t)blockIdx.y * 2 * a.n;
+  out[c] = sg;
+  out[a.n + c] = sb;
+}
+
+// ---- host --------------------------------------------------------------------
+
+// How a row of up to kRegN elements lies in registers: four elements a load where n allows it, else single elements; one wave up to
+// 1024 elements, four above.
+struct Form {
+  bool vec;
+  int wpr, nv;
+};
+Form form_of(int n) {
+  Form f;
+  f.vec = n % 4 == 0;
+  f.wpr = n <= 1024 ? 1 : 4;
+  const int per = 64 * f.wpr * (f.vec ? 4 : 1);
+  f.nv = (n + per - 1) / per;
+  if (!f.vec) f.nv = f.wpr == 4 ? 16 : f.nv <= 4 ? 4 : 16;
+  return f;
+}
+
+int64_t bwd_groups(int n, int64_t T) {
+  if (n > kRegN) return T < 16 ? (T ? 1 : 0) : (T / 16 < 64 ? T / 16 : 64);
+  const int rows = kBwdThreads / (64 * form_of(n).wpr);
+  const int64_t g = (T + rows - 1) / rows;
+  return g < kBwdGroups ? g : kBwdGroups;
+}
+
+ttc_status check(const ttc_norm_desc* d, int64_t T) {
+  if (!d) return TTC_ERR_NULL;
+  if (d->n < 1 || d->n > TTC_NORM_MAX_N) return TTC_ERR_SHAPE;
+  if (T < 0 || T > 0x7fffffff) return TTC_ERR_SHAPE;
+  if (!(d->eps >= 0.f)) return TTC_ERR_SHAPE;
+  if (d->x_dtype != TTC_F32 && d->x_dtype != TTC_BF16) return TTC_ERR_DTYPE;
+  if (d->y_dtype != TTC_F32 && d->y_dtype != TTC_BF16 && d->y_dtype != TTC_FP8) return TTC_ERR_DTYPE;
+  return TTC_OK;
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+size_t saved_need(int64_t T) { return (size_t)T * sizeof(float2); }
+size_t scratch_need(int n, int64_t T) { return (size_t)bwd_groups(n, T) * 2 * n * sizeof(float); }
+
+// f(TX{}, TY{}) for the descriptor's types
+template <typename F>
+void with_types(const ttc_norm_desc* d, F f) {
+  if (d->x_dtype == TTC_F32) {
+    if (d->y_dtype == TTC_F32) f(float{}, float{});
+    else if (d->y_dtype == TTC_BF16) f(float{}, bf16_t{});
+    else f(float{}, fp8_t{});
+  } else {
+    if (d->y_dtype == TTC_F32) f(bf16_t{}, float{});
+    else if (d->y_dtype == TTC_BF16) f(bf16_t{}, bf16_t{});
+    else f(bf16_t{}, fp8_t{});
+  }
+}
+
+// f(integral constants VE, WPR, NV) for a row's register form
+template <typename F>
+void with_form(const Form& m, F f) {
+  using std::integral_constant;
+#define TTC_NORM_FORM(VE, WPR, NV)                                       \
+  if (m.vec == (VE == 4) && m.wpr == WPR && m.nv == NV)                  \
+    return f(integral_constant<int, VE>{}, integral_constant<int, WPR>{}, integral_constant<int, NV>{})
+  TTC_NORM_FORM(4, 1, 1);
+  TTC_NORM_FORM(4, 1, 2);
+  TTC_NORM_FORM(4, 1, 3);
+  TTC_NORM_FORM(4, 1, 4);
+  TTC_NORM_FORM(4, 4, 2);
+  TTC_NORM_FORM(4, 4, 3);
+  TTC_NORM_FORM(4, 4, 4);
+  TTC_NORM_FORM(1, 1, 4);
+  TTC_NORM_FORM(1, 1, 16);
+  TTC_NORM_FORM(1, 4, 16);
+#undef TTC_NORM_FORM
+}
+
+ttc_status launched() { return hipGetLastError() == hipSuccess ? TTC_OK : TTC_ERR_HIP; }
+
+}  // namespace
+}  // namespace ttc
+
+using namespace ttc;
+
+extern "C" ttc_status ttc_norm_workspace(const ttc_norm_desc* desc, int64_t T, size_t* saved_bytes,
+                                         size_t* scratch_bytes) {
+  if (!saved_bytes || !scratch_bytes) return TTC_ERR_NULL;
+  const ttc_status st = check(desc, T);
+  if (st != TTC_OK) return st;
+  *saved_bytes = saved_need(T);
+  *scratch_bytes = scratch_need(desc->n, T);
+  return TTC_OK;
+}
+
+extern "C" ttc_status ttc_norm_fwd(const ttc_norm_desc* desc, int64_t T, const void* x, const void* res,
+                                   const float* gamma, const float* beta, void* h, void* y, void* saved,
+                                   size_t saved_bytes, ttc_stream_t stream) {
+  const ttc_status st = check(desc, T);
+  if (st != TTC_OK) return st;
+  if (T == 0) return TTC_OK;
+  if (!x || !gamma || !beta || !y || !saved || (res && !h)) return TTC_ERR_NULL;
+  if (!al16(x) || !al16(res) || !al16(gamma) || !al16(beta) || !al16(y) || !al16(saved) || (res && !al16(h)))
+    return TTC_ERR_ALIGN;
+  if (saved_bytes < saved_need(T)) return TTC_ERR_WORKSPACE;
+  NormArgs a = {};
+  a.x = x;
+  a.res = res;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.h = h;
+  a.y = y;
+  a.stats = static_cast<float2*>(saved);
+  a.T = T;
+  a.n = desc->n;
+  a.eps = desc->eps;
+  hipStream_t s = (hipStream_t)stream;
+  (void)hipGetLastError();
+  TraceScope ts("norm_fwd", s);
+  with_types(desc, [&](auto tx, auto ty) {
+    typedef decltype(tx) TX;
+    typedef decltype(ty) TY;
+    if (a.n > kRegN) {
+      auto kern = k_norm_fwd_long<TX, TY>;
+      TTC_LAUNCH(kern, dim3((unsigned)(T < 65536 ? T : 65536)), dim3(kLongThreads), 0, s, a);
+      return;
+    }
+    const Form m = form_of(a.n);
+    const int rows = kFwdThreads / (64 * m.wpr);
+    const int64_t g = (T + rows - 1) / rows;
+    const unsigned grid = (unsigned)(g < kFwdGroups ? g : kFwdGroups);
+    with_form(m, [&](auto ve, auto wpr, auto nv) {
+      auto kern = k_norm_fwd<TX, TY, decltype(ve)::value, decltype(wpr)::value, decltype(nv)::value>;
+      TTC_LAUNCH(kern, dim3(grid), dim3(kFwdThreads), 0, s, a);
+    });
+  });
+  return launched();
+}
+
+extern "C" ttc_status ttc_norm_bwd(const ttc_norm_desc* desc, int64_t T, const void* dy, const void* h,
+                                   const float* gamma, const void* dh, const void* saved, size_t saved_bytes, void* dx,
+                                   float* dgamma, float* dbeta, void* scratch, size_t scratch_bytes,
+                                   ttc_stream_t stream) {
+  const ttc_status st = check(desc, T);
+  if (st != TTC_OK) return st;
+  if (!dgamma || !dbeta) return TTC_ERR_NULL;
+  if (!al16(dgamma) || !al16(dbeta)) return TTC_ERR_ALIGN;
+  if (T > 0) {
+    if (!dy || !h || !gamma || !saved || !dx || !scratch) return TTC_ERR_NULL;
+    if (!al16(dy) || !al16(h) || !al16(gamma) || !al16(dh) || !al16(saved) || !al16(dx) || !al16(scratch))
+      return TTC_ERR_ALIGN;
+    if (saved_bytes < saved_need(T) || scratch_bytes < scratch_need(desc->n, T)) return TTC_ERR_WORKSPACE;
+  }
+  NormArgs a = {};
+  a.dy = dy;
+  a.h = const_cast<void*>(h);
+  a.gamma = gamma;
+  a.dh = dh;
+  a.y = dx;
+  a.stats = static_cast<float2*>(const_cast<void*>(saved));
+  a.part = static_cast<float*>(scratch);
+  a.T = T;
+  a.n = desc->n;
+  hipStream_t s = (hipStream_t)stream;
+  const int64_t groups = bwd_groups(a.n, T);
+  (void)hipGetLastError();
+  if (T > 0) {
+    with_types(desc, [&](auto tx, auto ty) {
+      typedef decltype(tx) TX;
+      typedef decltype(ty) TY;
+      if (a.n > kRegN) {
+        {
+          TraceScope ts("norm_bwd", s);
+          auto kern = k_norm_dx_long<TX, TY>;
+          TTC_LAUNCH(kern, dim3((unsigned)(T < 65536 ? T : 65536)), dim3(kLongThreads), 0, s, a);
+        }
+        TraceScope ts("norm_dw", s);
+        auto kern = k_norm_dw_long<TX, TY>;
+        TTC_LAUNCH(kern, dim3((unsigned)((a.n + kLongCols - 1) / kLongCols), (unsigned)groups), dim3(kLongCols), 0, s,
+                   a);
+        return;
+      }
+      const Form m = form_of(a.n);
+      const size_t lds = (size_t)(kBwdThreads / (64 * m.wpr)) * a.n * sizeof(float);  // at most 64 KB
+      TraceScope ts("norm_bwd", s);
+      with_form(m, [&](auto ve, auto wpr, auto nv) {
+        auto kern = k_norm_bwd<TX, TY, decltype(ve)::value, decltype(wpr)::value, decltype(nv)::value>;
+        TTC_LAUNCH(kern, dim3((unsigned)groups), dim3(kBwdThreads), lds, s, a);
+      });
+    });
+  }
+  TraceScope ts("norm_reduce", s);
+  TTC_LAUNCH(k_norm_reduce, dim3((unsigned)((2 * (int64_t)a.n + 63) / 64)), dim3(1024), 0, s, a.part, (int)groups, a.n,
+             dgamma, dbeta);
+  return launched();
+}
