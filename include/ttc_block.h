@@ -73,6 +73,89 @@ ttc_status ttc_norm_bwd(const ttc_norm_desc* desc, int64_t T, const void* dy,
                         float* dgamma, float* dbeta, void* scratch,
                         size_t scratch_bytes, ttc_stream_t stream);
 
+/* ---- attention over a sliding window with sinks --------------------------- */
+
+/* q, o and their gradients hold a row of heads * dim elements per token, k, v
+ * and theirs one of kv_heads * dim; query head h reads key head
+ * h / (heads / kv_heads).  With p = i + (lk - lq) the place of query i of a
+ * sequence among its keys (the queries stand at the keys' end), key j is seen
+ * if j <= p + right and (j >= p - left or j < sinks). */
+typedef struct {
+  int32_t heads;    /* 1 .. 4096, a multiple of kv_heads                   */
+  int32_t kv_heads; /* >= 1                                                */
+  int32_t dim;      /* elements of a head, a multiple of 8 up to 128       */
+  int32_t left;     /* keys before a query's own that it sees; < 0: all    */
+  int32_t right;    /* keys after a query's own that it sees; < 0: all     */
+  int32_t sinks;    /* first keys of a sequence that the left side keeps   */
+  int32_t dtype;    /* TTC_F32 or TTC_BF16: q, k, v, o and the gradients   */
+  float scale;      /* of the scores: 1 / sqrt(dim) as a rule              */
+} ttc_attn_desc;
+
+/* The sequences of a call.  Offsets (device, batch + 1 ascending int32 each)
+ * give where a packed sequence's rows begin; both NULL: every sequence has
+ * tq / batch queries and tk / batch keys.  Offsets are cut to [0, tq] and
+ * [0, tk] and to ascending order, so wrong ones touch no other memory; rows of
+ * no sequence are not written.  max_q and max_k say how many work-groups are
+ * worth launching with offsets; results do not depend on them. */
+typedef struct {
+  int32_t batch;
+  int32_t reserved;         /* 0                                            */
+  int64_t tq, tk;           /* rows of q and of k, at most 2^28             */
+  int64_t max_q, max_k;     /* rows of the longest sequence, 0: not known   */
+  const int32_t* q_offsets; /* or NULL                                      */
+  const int32_t* k_offsets; /* or NULL                                      */
+} ttc_attn_seqs;
+
+/* Bytes of saved (the scores' log-sum of each row and head, written by the
+ * forward, read by the backward) and of the backward's scratch.  Host-only;
+ * the offsets are not read. */
+ttc_status ttc_attn_workspace(const ttc_attn_desc* desc,
+                              const ttc_attn_seqs* seqs, size_t* saved_bytes,
+                              size_t* scratch_bytes);
+
+/*
+ * Forward: o_i = sum_j P_ij v_j, P_i = softmax over the seen keys of
+ * scale q_i . k_j.  A query that sees no key, or whose scores are all minus
+ * infinity, gets zeros.  What a query does not see (a NaN, an infinity) does
+ * not reach it.
+ *   q - tq rows;  k, v - tk rows;  o - tq rows, overwritten
+ */
+ttc_status ttc_attn_fwd(const ttc_attn_desc* desc, const ttc_attn_seqs* seqs,
+                        const void* q, const void* k, const void* v, void* o,
+                        void* saved, size_t saved_bytes, ttc_stream_t stream);
+
+/*
+ * Backward: the gradients of sum(d_o . o).  q, k, v, o, saved as in the
+ * forward; dq (tq rows), dk and dv (tk rows) are overwritten; a key head's
+ * gradients are the sums over its query heads.  Rows that see, or are seen by,
+ * nothing get zeros.
+ */
+ttc_status ttc_attn_bwd(const ttc_attn_desc* desc, const ttc_attn_seqs* seqs,
+                        const void* q, const void* k, const void* v,
+                        const void* o, const void* d_o, const void* saved,
+                        size_t saved_bytes, void* dq, void* dk, void* dv,
+                        void* scratch, size_t scratch_bytes,
+                        ttc_stream_t stream);
+
+/* Bytes of the scratch of ttc_attn_decode.  Host-only. */
+ttc_status ttc_attn_decode_workspace(const ttc_attn_desc* desc, int64_t batch,
+                                     int64_t capacity, size_t* scratch_bytes);
+
+/*
+ * One new token for each of `batch` sequences over their caches.  The query
+ * stands at the last of its sequence's lens[b] keys (its own, written before
+ * the call); the cache's rows from lens[b] on are not used, whatever they
+ * hold.
+ *   q, o - batch rows of heads * dim
+ *   k, v - batch x capacity rows of kv_heads * dim, capacity at most 2^28
+ *   lens - batch int32 (device), cut to [0, capacity]; 0 gives zeros
+ */
+ttc_status ttc_attn_decode(const ttc_attn_desc* desc, int64_t batch,
+                           int64_t capacity, const void* q, const void* k,
+                           const void* v, const int32_t* lens, void* o,
+                           void* scratch, size_t scratch_bytes,
+                           ttc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -67,6 +67,11 @@ EXPORTS = [
     "ttc_norm_workspace",
     "ttc_norm_fwd",
     "ttc_norm_bwd",
+    "ttc_attn_workspace",
+    "ttc_attn_fwd",
+    "ttc_attn_bwd",
+    "ttc_attn_decode_workspace",
+    "ttc_attn_decode",
 ]
 
 
@@ -118,6 +123,32 @@ class NormDesc(ctypes.Structure):
     ]
 
 
+class AttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("left", ctypes.c_int32),
+        ("right", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class AttnSeqs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("tq", ctypes.c_int64),
+        ("tk", ctypes.c_int64),
+        ("max_q", ctypes.c_int64),
+        ("max_k", ctypes.c_int64),
+        ("q_offsets", ctypes.c_void_p),
+        ("k_offsets", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -135,6 +166,8 @@ def lib() -> ctypes.CDLL:
     D = ctypes.POINTER(TTLinearDesc)
     E = ctypes.POINTER(TTMEmbedDesc)
     N = ctypes.POINTER(NormDesc)
+    A = ctypes.POINTER(AttnDesc)
+    S = ctypes.POINTER(AttnSeqs)
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "tt_linear_workspace": [D, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
@@ -169,6 +202,11 @@ def lib() -> ctypes.CDLL:
         "ttc_norm_workspace": [N, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
         "ttc_norm_fwd": [N, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
         "ttc_norm_bwd": [N, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _SZ, _P],
+        "ttc_attn_workspace": [A, S, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+        "ttc_attn_fwd": [A, S, _P, _P, _P, _P, _P, _SZ, _P],
+        "ttc_attn_bwd": [A, S, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _SZ, _P],
+        "ttc_attn_decode_workspace": [A, _I64, _I64, ctypes.POINTER(_SZ)],
+        "ttc_attn_decode": [A, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -465,6 +503,48 @@ def ttc_norm_bwd(desc, T, dy, h, gamma, dh, saved, saved_bytes, dx, dgamma, dbet
     _check("ttc_norm_bwd", code)
 
 
+def make_attn_desc(heads, dim, kv_heads=None, left=-1, right=0, sinks=0, dtype=TTC_F32, scale=None):
+    """left, right: keys that a query sees on either side of its own, -1: all."""
+    kv_heads = heads if kv_heads is None else kv_heads
+    scale = (dim ** -0.5 if dim > 0 else 1.0) if scale is None else scale
+    return AttnDesc(int(heads), int(kv_heads), int(dim), int(left), int(right), int(sinks), int(dtype), float(scale))
+
+
+def make_attn_seqs(batch, tq, tk, q_offsets=None, k_offsets=None, max_q=0, max_k=0):
+    """q_offsets, k_offsets: device addresses of batch + 1 int32, or None."""
+    return AttnSeqs(int(batch), 0, int(tq), int(tk), int(max_q), int(max_k), q_offsets, k_offsets)
+
+
+def ttc_attn_workspace(desc: AttnDesc, seqs: AttnSeqs):
+    s, c = _SZ(0), _SZ(0)
+    _check("ttc_attn_workspace",
+           lib().ttc_attn_workspace(ctypes.byref(desc), ctypes.byref(seqs), ctypes.byref(s), ctypes.byref(c)))
+    return s.value, c.value
+
+
+def ttc_attn_fwd(desc, seqs, q, k, v, o, saved, saved_bytes, stream=0):
+    code = lib().ttc_attn_fwd(ctypes.byref(desc), ctypes.byref(seqs), q, k, v, o, saved, saved_bytes, stream)
+    _check("ttc_attn_fwd", code)
+
+
+def ttc_attn_bwd(desc, seqs, q, k, v, o, d_o, saved, saved_bytes, dq, dk, dv, scratch, scratch_bytes, stream=0):
+    code = lib().ttc_attn_bwd(ctypes.byref(desc), ctypes.byref(seqs), q, k, v, o, d_o, saved, saved_bytes, dq, dk, dv,
+                              scratch, scratch_bytes, stream)
+    _check("ttc_attn_bwd", code)
+
+
+def ttc_attn_decode_workspace(desc: AttnDesc, batch: int, capacity: int):
+    c = _SZ(0)
+    _check("ttc_attn_decode_workspace",
+           lib().ttc_attn_decode_workspace(ctypes.byref(desc), batch, capacity, ctypes.byref(c)))
+    return c.value
+
+
+def ttc_attn_decode(desc, batch, capacity, q, k, v, lens, o, scratch, scratch_bytes, stream=0):
+    code = lib().ttc_attn_decode(ctypes.byref(desc), batch, capacity, q, k, v, lens, o, scratch, scratch_bytes, stream)
+    _check("ttc_attn_decode", code)
+
+
 def trace_start():
     _check("ttc_trace_start", lib().ttc_trace_start())
 
@@ -499,4 +579,4 @@ from .torch_api import (  # noqa: E402,F401
     rank_grads_batch,
     prepare_batch,
 )
-from .block_api import LayerNorm  # noqa: E402,F401
+from .block_api import LayerNorm, WindowAttention  # noqa: E402,F401

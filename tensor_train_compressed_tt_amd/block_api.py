@@ -8,7 +8,14 @@ from __future__ import annotations
 import torch
 
 from . import (
+    make_attn_desc,
+    make_attn_seqs,
     make_norm_desc,
+    ttc_attn_bwd,
+    ttc_attn_decode,
+    ttc_attn_decode_workspace,
+    ttc_attn_fwd,
+    ttc_attn_workspace,
     ttc_norm_bwd,
     ttc_norm_fwd,
     ttc_norm_workspace,
@@ -92,3 +99,103 @@ class LayerNorm:
                      _nbytes(saved), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), scratch.data_ptr(),
                      _nbytes(scratch), _stream())
         return dx, dgamma, dbeta
+
+
+class WindowAttention:
+    """Softmax attention over a sliding window with sinks.
+
+    ``window`` = (left, right): keys that a query sees before and after its own
+    place, -1 for all of a side ((-1, -1): full attention, (-1, 0): causal).
+    The first ``sinks`` keys of a sequence stay visible however far back they
+    are.  Queries stand at the end of their sequence's keys.  Query heads share
+    key heads in runs of heads / kv_heads.  q and o are (tokens, heads * dim),
+    k and v (tokens, kv_heads * dim), float32 or bfloat16; scores are scaled by
+    ``scale`` (1 / sqrt(dim) if None).
+    """
+
+    def __init__(self, heads, dim, kv_heads=None, window=(-1, -1), sinks=0, dtype=torch.float32, scale=None):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"no attention in {dtype}")
+        self.heads, self.dim = int(heads), int(dim)
+        self.kv_heads = self.heads if kv_heads is None else int(kv_heads)
+        self.dtype = dtype
+        self.desc = make_attn_desc(self.heads, self.dim, self.kv_heads, window[0], window[1], sinks, _ACT[dtype], scale)
+
+    def _seqs(self, q, k, batch, q_offsets, k_offsets, max_q, max_k):
+        """Sequences of one length each (``batch`` of them, no offsets) or packed
+        ones: int32 device offsets of batch + 1 row numbers."""
+        tq, tk, batch = int(q.shape[0]), int(k.shape[0]), int(batch)
+        if (q_offsets is None) != (k_offsets is None):
+            raise ValueError("q_offsets and k_offsets come together")
+        if q_offsets is None:
+            return make_attn_seqs(batch, tq, tk)
+        for t, name in ((q_offsets, "q_offsets"), (k_offsets, "k_offsets")):
+            _need(t, name, torch.int32, (batch + 1,))
+        if max_k is None and k_offsets is q_offsets:
+            max_k = max_q
+        return make_attn_seqs(batch, tq, tk, q_offsets.data_ptr(), k_offsets.data_ptr(), max_q or 0, max_k or 0)
+
+    def _need_qkv(self, q, k, v):
+        _need(q, "q", self.dtype, (q.shape[0], self.heads * self.dim))
+        _need(k, "k", self.dtype, (k.shape[0], self.kv_heads * self.dim))
+        _need(v, "v", self.dtype, tuple(k.shape))
+
+    def workspace(self, q, k, batch=1):
+        """Bytes of (saved, scratch) for these queries and keys."""
+        return ttc_attn_workspace(self.desc, make_attn_seqs(batch, int(q.shape[0]), int(k.shape[0])))
+
+    def forward(self, q, k, v, batch=1, q_offsets=None, k_offsets=None, max_q=None, out=None, saved=None):
+        """(o, saved).  ``max_q``, the longest sequence's queries, sizes the launch
+        of packed sequences; results do not depend on it."""
+        self._need_qkv(q, k, v)
+        seqs = self._seqs(q, k, batch, q_offsets, k_offsets, max_q, None)
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, "out", self.dtype, tuple(q.shape))
+        if saved is None:
+            saved = _bytes(ttc_attn_workspace(self.desc, seqs)[0], q.device)
+        _need_buf(saved, "saved")
+        ttc_attn_fwd(self.desc, seqs, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), saved.data_ptr(),
+                     _nbytes(saved), _stream())
+        return out, saved
+
+    def backward(self, q, k, v, o, do, saved, batch=1, q_offsets=None, k_offsets=None, max_q=None, max_k=None, dq=None,
+                 dk=None, dv=None, scratch=None):
+        """(dq, dk, dv); a key head's gradients are summed over its query heads."""
+        self._need_qkv(q, k, v)
+        seqs = self._seqs(q, k, batch, q_offsets, k_offsets, max_q, max_k)
+        _need(o, "o", self.dtype, tuple(q.shape))
+        _need(do, "do", self.dtype, tuple(q.shape))
+        _need_buf(saved, "saved")
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        _need(dq, "dq", self.dtype, tuple(q.shape))
+        _need(dk, "dk", self.dtype, tuple(k.shape))
+        _need(dv, "dv", self.dtype, tuple(k.shape))
+        if scratch is None:
+            scratch = _bytes(ttc_attn_workspace(self.desc, seqs)[1], q.device)
+        _need_buf(scratch, "scratch")
+        ttc_attn_bwd(self.desc, seqs, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                     saved.data_ptr(), _nbytes(saved), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), scratch.data_ptr(),
+                     _nbytes(scratch), _stream())
+        return dq, dk, dv
+
+    def decode(self, q, k, v, lens, out=None, scratch=None):
+        """o for one new token of each sequence: q (batch, heads * dim), the caches
+        k and v (batch, capacity, kv_heads * dim), ``lens`` int32 rows in use (the
+        new token's own among them); the window's right side has no meaning here."""
+        batch, capacity = int(q.shape[0]), int(k.shape[1])
+        _need(q, "q", self.dtype, (batch, self.heads * self.dim))
+        _need(k, "k", self.dtype, (batch, capacity, self.kv_heads * self.dim))
+        _need(v, "v", self.dtype, tuple(k.shape))
+        _need(lens, "lens", torch.int32, (batch,))
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, "out", self.dtype, tuple(q.shape))
+        if scratch is None:
+            scratch = _bytes(ttc_attn_decode_workspace(self.desc, batch, capacity), q.device)
+        _need_buf(scratch, "scratch")
+        ttc_attn_decode(self.desc, batch, capacity, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(),
+                        out.data_ptr(), scratch.data_ptr(), _nbytes(scratch), _stream())
+        return out

@@ -45,3 +45,45 @@ def test_norm_errors_before_launch():
     assert _code(lambda: call(dh=8)) == 5
     assert _code(lambda: call(saved_bytes=s - 1)) == 6 and _code(lambda: call(scratch_bytes=c - 1)) == 6
     ttc.ttc_norm_fwd(d, 0, None, None, None, None, None, None, None, 0)  # no rows: nothing is touched
+
+
+@pytest.mark.parametrize("kw,code", [(dict(heads=0), 2), (dict(heads=6, kv_heads=4), 2), (dict(kv_heads=0), 2), (dict(heads=4097), 2),
+                                     (dict(dim=0), 2), (dict(dim=12), 2), (dict(dim=136), 2), (dict(sinks=-1), 2),
+                                     (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(dtype=ttc.TTC_FP8), 4)])
+def test_attention_descriptors(kw, code):
+    d = ttc.make_attn_desc(**{"heads": 8, "dim": 64, **kw})
+    assert _code(ttc.ttc_attn_workspace, d, ttc.make_attn_seqs(1, 64, 64)) == code
+    assert _code(ttc.ttc_attn_decode_workspace, d, 2, 64) == code
+
+
+@pytest.mark.parametrize("kw,code", [(dict(batch=0), 2), (dict(batch=3), 2), (dict(tq=-1), 2), (dict(tk=(1 << 28) + 1), 2),
+                                     (dict(max_q=-1), 2), (dict(q_offsets=16), 1), (dict(batch=1 << 21, tq=0, tk=0), 7)])
+def test_attention_sequences(kw, code):
+    d = ttc.make_attn_desc(8, 64)
+    assert _code(ttc.ttc_attn_workspace, d, ttc.make_attn_seqs(**{"batch": 2, "tq": 64, "tk": 64, **kw})) == code
+
+
+def test_attention_errors_before_launch():
+    d, seqs = ttc.make_attn_desc(8, 64, 4, 10, 0, 2, ttc.TTC_BF16), ttc.make_attn_seqs(2, 64, 96)
+    s, c = ttc.ttc_attn_workspace(d, seqs)
+    fwd = dict(q=16, k=16, v=16, o=16, saved=16, saved_bytes=s)
+    call = lambda **kw: ttc.ttc_attn_fwd(d, seqs, **{**fwd, **kw})  # noqa: E731
+    for k in ("q", "k", "v", "o", "saved"):
+        assert _code(lambda: call(**{k: None})) == 1, k
+        assert _code(lambda: call(**{k: 24})) == 5, k
+    assert _code(lambda: call(saved_bytes=s - 1)) == 6
+    bwd = dict(q=16, k=16, v=16, o=16, d_o=16, saved=16, saved_bytes=s, dq=16, dk=16, dv=16, scratch=16, scratch_bytes=c)
+    call = lambda **kw: ttc.ttc_attn_bwd(d, seqs, **{**bwd, **kw})  # noqa: E731
+    for k in ("q", "k", "v", "o", "d_o", "saved", "dq", "dk", "dv", "scratch"):
+        assert _code(lambda: call(**{k: None})) == 1, k
+        assert _code(lambda: call(**{k: 24})) == 5, k
+    assert _code(lambda: call(saved_bytes=s - 1)) == 6 and _code(lambda: call(scratch_bytes=c - 1)) == 6
+    dec = dict(q=16, k=16, v=16, lens=16, o=16, scratch=16, scratch_bytes=1 << 40)
+    call = lambda **kw: ttc.ttc_attn_decode(d, 2, 64, **{**dec, **kw})  # noqa: E731
+    for k in ("q", "k", "v", "lens", "o"):
+        assert _code(lambda: call(**{k: None})) == 1, k
+        assert _code(lambda: call(**{k: 24})) == 5, k
+    assert _code(ttc.ttc_attn_decode_workspace, d, -1, 64) == 2 and _code(ttc.ttc_attn_decode_workspace, d, 1, (1 << 28) + 1) == 2
+    ttc.ttc_attn_fwd(d, ttc.make_attn_seqs(1, 0, 0), None, None, None, None, None, 0)  # no rows: nothing is touched
+    ttc.ttc_attn_bwd(d, ttc.make_attn_seqs(1, 0, 0), None, None, None, None, None, None, 0, None, None, None, None, 0)
+    ttc.ttc_attn_decode(d, 0, 64, None, None, None, None, None, None, 0)

@@ -1,0 +1,434 @@
+"""GPU parity of sliding-window attention with sinks against its formulas in 64 bits.
+
+Tolerances, element by element.  u is half a step of the type (2^-8 bf16, 2^-24
+fp32).  A score is an fp32 sum of at most 128 products whose magnitudes add up to
+at most A: 64 fp32 steps of 1 + A cover it, the exponential and the statistics,
+so P is off by f = 64 2^-24 (1 + A) of itself.  P and dS enter the products
+rounded to the type.  So
+  o:      u |o| + (u + f) sum P |v|                                  (= eo)
+  delta:  sum |do| eo + 64 2^-24 sum |do| |o|                        (= ed)
+  dS:     P (f |dP - delta| + 64 2^-24 sum |do| |v| + ed) + u |dS|    (= es)
+  dq, dk: u |.| + scale sum (es + 64 2^-24 |dS|) |k or q|
+  dv:     u |dv| + sum P (u + f) |do|
+"""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+E32 = 2.0 ** -24
+STEPS = 64 * E32
+
+
+def _ttc():
+    import tensor_train_compressed_tt_amd as ttc
+    return ttc
+
+
+def _seen(lq, lk, left, right, sinks, dev):
+    p = torch.arange(lq, device=dev)[:, None] + (lk - lq)
+    j = torch.arange(lk, device=dev)[None, :]
+    m = torch.ones((lq, lk), dtype=torch.bool, device=dev)
+    if right >= 0:
+        m &= j <= p + right
+    if left >= 0:
+        m &= (j >= p - left) | (j < sinks)
+    return m
+
+
+def _reference(q, k, v, do, m, scale, u, group):
+    """One sequence; q, do (lq, h, d), k, v (lk, hk, d).  Values and bounds."""
+    q, k, v, do = (t.double().transpose(0, 1).contiguous() for t in (q, k, v, do))
+    kw, vw = k.repeat_interleave(group, 0), v.repeat_interleave(group, 0)
+    tr = lambda x: x.transpose(1, 2).contiguous()  # noqa: E731
+    s = torch.where(m, q @ tr(kw) * scale, -math.inf)
+    top = s.amax(2, keepdim=True) if s.shape[2] else s.new_full((*s.shape[:2], 1), -math.inf)
+    top = torch.where(top == -math.inf, 0.0, top)
+    e = (s - top).exp()
+    total = e.sum(2, keepdim=True)
+    p = e / torch.where(total == 0, 1.0, total)
+    big = (q.abs() @ tr(kw).abs() * abs(scale)) * m
+    f = STEPS * (1 + (big.amax(2, keepdim=True) if s.shape[2] else 0))
+    o = p @ vw
+    eo = u * o.abs() + (p * (u + f)) @ vw.abs()
+    dp, delta = do @ tr(vw), (do * o).sum(2, keepdim=True)
+    ds = p * (dp - delta)
+    ed = (do.abs() * eo).sum(2, keepdim=True) + STEPS * (do * o).abs().sum(2, keepdim=True)
+    es = p * (f * (dp - delta).abs() + STEPS * (do.abs() @ tr(vw).abs()) + ed) + (u + STEPS) * ds.abs()
+    narrow = lambda x: x.view(k.shape[0], group, *x.shape[1:]).sum(1)  # noqa: E731
+    dq, dk, dv = scale * ds @ kw, narrow(scale * tr(ds) @ q), narrow(tr(p) @ do)
+    eq = u * dq.abs() + abs(scale) * es @ kw.abs()
+    ek = u * dk.abs() + narrow(abs(scale) * tr(es) @ q.abs())
+    ev = u * dv.abs() + narrow(tr(p * (u + f)) @ do.abs())
+    return [tuple(x.transpose(0, 1) for x in y) for y in ((o, eo), (dq, eq), (dk, ek), (dv, ev))]
+
+
+def _close(got, ref, bound, what):
+    off = (got.double() - ref).abs() - bound
+    assert bool((off <= 1e-30).all()), f"{what}: {float(off.nan_to_num(math.inf).max()):.3g} over its bound"
+
+
+def _inputs(lq, lk, h, hk, d, ty, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda t, w: torch.randn(sum(t), w * d, generator=g)  # noqa: E731
+    return [x.to(ty).cuda() for x in (size * r(lq, h), r(lk, hk), r(lk, hk), r(lq, h))]
+
+
+def _offsets(lens):
+    return torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
+
+
+def _check(lq, lk, h=2, hk=None, d=64, window=(-1, -1), sinks=0, ty=BF16, seed=0, packed=True, size=1.0, scale=None, max_q=None,
+           max_k=None):
+    ttc = _ttc()
+    hk = hk or h
+    q, k, v, do = _inputs(lq, lk, h, hk, d, ty, seed, size)
+    layer = ttc.WindowAttention(h, d, hk, window=window, sinks=sinks, dtype=ty, scale=scale)
+    kw = dict(batch=len(lq))
+    if packed:
+        kw |= dict(q_offsets=_offsets(lq), k_offsets=_offsets(lk), max_q=max_q)
+    o, saved = layer.forward(q, k, v, **kw)
+    dq, dk, dv = layer.backward(q, k, v, o, do, saved, max_k=max_k, **kw)
+    torch.cuda.synchronize()
+    u = torch.finfo(ty).eps / 2
+    iq = ik = 0
+    for a, b in zip(lq, lk):
+        m = _seen(a, b, *window, sinks, "cuda")
+        cut = lambda t, i, n, w: t[i:i + n].view(n, w, d)  # noqa: E731
+        ref = _reference(cut(q, iq, a, h), cut(k, ik, b, hk), cut(v, ik, b, hk), cut(do, iq, a, h), m,
+                         layer.desc.scale, u, h // hk)
+        got = cut(o, iq, a, h), cut(dq, iq, a, h), cut(dk, ik, b, hk), cut(dv, ik, b, hk)
+        for name, x, (y, bound) in zip(("o", "dq", "dk", "dv"), got, ref):
+            _close(x, y, bound, f"{name} of {a} queries, {b} keys")
+        iq, ik = iq + a, ik + b
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("d", [8, 16, 24, 32, 40, 64, 72, 80, 96, 104, 128])
+def test_dims(ty, d):
+    _check([150], [150], d=d, window=(40, 9), sinks=3, ty=ty, seed=d)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 192, 255, 256, 257, 385, 1000])
+@pytest.mark.parametrize("window,sinks", [((-1, -1), 0), ((-1, 0), 0), ((32, 32), 1)])
+def test_lengths(n, ty, window, sinks):
+    _check([n, n], [n, n], window=window, sinks=sinks, ty=ty, seed=n, packed=False)
+
+
+@pytest.mark.parametrize("window", [(0, 0), (0, -1), (-1, 5), (1, 0), (3, 5), (31, 0), (63, 64), (64, 63), (100, 1), (200, 0), (5, 200),
+                                    (1 << 30, 1 << 30), (2 ** 31 - 1, 0)])
+@pytest.mark.parametrize("sinks", [0, 1, 4, 33, 64, 100, 129, 500, 2 ** 31 - 1])
+def test_windows(window, sinks):
+    _check([300], [300], h=1, window=window, sinks=sinks, seed=sinks % 97 + window[0] % 89)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("lq,lk", [(1, 200), (7, 200), (64, 130), (129, 130), (100, 700), (130, 129), (200, 70), (300, 1)])
+@pytest.mark.parametrize("window,sinks", [((-1, 0), 0), ((16, 0), 4), ((20, 7), 2), ((-1, -1), 0)])
+def test_fewer_queries_than_keys_and_more(lq, lk, ty, window, sinks):
+    """Queries stand at the keys' end; with more queries than keys the first ones see nothing or only what lies ahead."""
+    _check([lq], [lk], window=window, sinks=sinks, ty=ty, seed=lq + lk)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("h,hk", [(1, 1), (4, 1), (6, 2), (12, 3), (8, 8)])
+def test_shared_key_heads(h, hk, ty):
+    _check([150, 3], [150, 3], h=h, hk=hk, d=32, window=(30, 30), sinks=2, ty=ty, seed=h)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("window,sinks", [((-1, -1), 0), ((50, 0), 4), ((64, 64), 1)])
+def test_packed(ty, window, sinks):
+    lens = [130, 0, 1, 64, 257, 0, 31, 128, 2]
+    _check(lens, lens, h=4, hk=2, window=window, sinks=sinks, ty=ty, max_q=257)
+    _check(lens, [0, 5, 1, 200, 257, 3, 30, 129, 0], h=2, window=window, sinks=sinks, ty=ty, seed=1)
+
+
+@pytest.mark.parametrize("longest", [1, 100, 5000, 1 << 40])
+def test_longest_sequence_is_a_hint(longest):
+    _check([300, 2, 129], [300, 2, 129], window=(40, 40), sinks=1, max_q=longest, max_k=longest)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+def test_long(ty):
+    _check([3000], [3000], h=2, hk=1, window=(400, 17), sinks=5, ty=ty)
+    _check([2100], [2100], h=1, window=(-1, 0), ty=ty)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+def test_large_scores(ty):
+    """Scores of some hundreds: P is one key's, and nothing overflows."""
+    _check([200], [200], window=(60, 60), sinks=1, ty=ty, size=60.0)
+    _check([200], [200], window=(60, 0), ty=ty, size=8.0, scale=-1.0)
+
+
+def test_scores_that_are_all_minus_infinity():
+    ttc = _ttc()
+    for ty in (F32, BF16):
+        q, k, v, do = _inputs([70], [70], 1, 1, 32, ty, 0)
+        q[5] = 1.0
+        k[:] = 0.0
+        k[:, 3] = -math.inf
+        q[:, 3] = 1.0
+        o, saved = ttc.WindowAttention(1, 32, window=(-1, 0), dtype=ty).forward(q, k, v)
+        assert not bool(o.any())
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n,window,sinks", [(100, (10, 3), 2), (300, (-1, 0), 0), (700, (64, 64), 1), (128, (0, 0), 0)])
+def test_what_is_not_seen_does_not_count(ty, bad, n, window, sinks):
+    """NaN and infinities in keys, values and queries: rows that do not see them keep their bits."""
+    ttc = _ttc()
+    h, hk, d = 4, 2, 64
+    layer = ttc.WindowAttention(h, d, hk, window=window, sinks=sinks, dtype=ty)
+    m = _seen(n, n, *window, sinks, "cuda")
+    for which in ("q", "k", "v", "do"):
+        t = dict(zip(("q", "k", "v", "do"), _inputs([n], [n], h, hk, d, ty, 3)))
+
+        def go():
+            o, saved = layer.forward(t["q"], t["k"], t["v"])
+            return (o,) + layer.backward(t["q"], t["k"], t["v"], o, t["do"], saved)
+
+        clean = go()
+        rows = [n // 2, n - 1]
+        t[which][rows] = bad
+        got = go()
+        if which in ("k", "v"):
+            hit_q = m[:, rows].any(1)  # queries that see a bad row
+            hit_k = m[hit_q].any(0)  # keys that such queries see
+            hit_k[rows] = True
+        else:
+            hit_q = torch.zeros(n, dtype=torch.bool, device="cuda")
+            hit_q[rows] = True
+            hit_k = m[hit_q].any(0)
+        for name, a, b, hit in zip(("o", "dq", "dk", "dv"), clean, got, (hit_q, hit_q, hit_k, hit_k)):
+            assert bool(torch.isfinite(b[~hit]).all()), (which, name)
+            # the same values up to the rounding of another order of sums
+            torch.testing.assert_close(b[~hit].float(), a[~hit].float(), rtol=4 * torch.finfo(ty).eps, atol=8 * torch.finfo(ty).eps)
+        if which == "v":
+            assert not bool(torch.isfinite(got[0][hit_q]).any(1).all()), "a seen bad value has to show"
+
+
+def test_gradient_is_the_difference_quotient():
+    """fp32, 9 queries and keys: central differences of sum(do . o) with a step of
+    2^-6; their own error is step^2 / 6 times the third derivative (of order 1
+    here), plus the rounding of a sum of 9 * 8 values over the step."""
+    ttc = _ttc()
+    q, k, v, do = _inputs([9], [9], 2, 1, 8, F32, 4)
+    layer = ttc.WindowAttention(2, 8, 1, window=(4, 1), sinks=1, dtype=F32)
+    f = lambda: float((layer.forward(q, k, v)[0].double() * do.double()).sum())  # noqa: E731
+    o, saved = layer.forward(q, k, v)
+    grads = layer.backward(q, k, v, o, do, saved)
+    step = 2.0 ** -6
+    for t, grad in zip((q, k, v), grads):
+        flat, got = t.view(-1), grad.view(-1)
+        for i in range(0, flat.numel(), 7):
+            was = float(flat[i])
+            flat[i] = was + step
+            hi, up = f(), float(flat[i])
+            flat[i] = was - step
+            lo, down = f(), float(flat[i])
+            flat[i] = was
+            assert abs((hi - lo) / (up - down) - float(got[i])) < 5e-3
+
+
+def _decode_check(lens, cap, h=4, hk=2, d=64, left=-1, sinks=0, ty=BF16, seed=0):
+    ttc = _ttc()
+    b = len(lens)
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(b, h * d, generator=g).to(ty).cuda()
+    k, v = (torch.randn(b, cap, hk * d, generator=g).to(ty).cuda() for _ in range(2))
+    for i, n in enumerate(lens):  # what a cache holds past its end counts for nothing
+        k[i, max(n, 0):], v[i, max(n, 0):] = float("nan"), float("inf")
+    o = ttc.WindowAttention(h, d, hk, window=(left, 0), sinks=sinks, dtype=ty).decode(
+        q, k, v, torch.tensor(lens, dtype=torch.int32).cuda())
+    u = torch.finfo(ty).eps / 2
+    for i, n in enumerate(lens):
+        n = min(max(n, 0), cap)
+        if n == 0:
+            assert not bool(o[i].any())
+            continue
+        m = _seen(1, n, left, 0, sinks, "cuda")
+        qi = q[i].view(1, h, d)
+        (y, bound), *_ = _reference(qi, k[i, :n].view(n, hk, d), v[i, :n].view(n, hk, d), qi, m, d ** -0.5, u, h // hk)
+        _close(o[i].view(1, h, d), y, bound, f"o over {n} keys")
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("d", [8, 32, 40, 64, 80, 96, 128])
+def test_decode_dims(ty, d):
+    _decode_check([1, 100, 77], 100, d=d, ty=ty, seed=d)
+
+
+@pytest.mark.parametrize("left,sinks", [(-1, 0), (0, 0), (0, 3), (63, 4), (127, 0), (511, 64), (100, 100), (4000, 2), (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("ty", [F32, BF16])
+def test_decode_windows(left, sinks, ty):
+    _decode_check([0, 1, 2, 63, 64, 65, 128, 300, 1000, 1537, 2000], 2000, left=left, sinks=sinks, ty=ty)
+
+
+@pytest.mark.parametrize("h,hk", [(1, 1), (8, 1), (12, 4), (5, 5), (64, 4), (33, 1)])
+def test_decode_heads(h, hk):
+    _decode_check([700, 31], 701, h=h, hk=hk)
+    _decode_check([700, 31], 701, h=h, hk=hk, d=128, left=200, sinks=9, ty=F32)
+
+
+def test_decode_lengths_are_cut():
+    _decode_check([-5, 9, 3], 8)
+
+
+def test_decode_what_is_not_seen_does_not_count():
+    ttc = _ttc()
+    b, cap, n = 2, 900, 800
+    for ty in (F32, BF16):
+        g = torch.Generator().manual_seed(1)
+        q = torch.randn(b, 4 * 64, generator=g).to(ty).cuda()
+        k, v = (torch.randn(b, cap, 2 * 64, generator=g).to(ty).cuda() for _ in range(2))
+        lens = torch.tensor([n, 5], dtype=torch.int32).cuda()
+        layer = ttc.WindowAttention(4, 64, 2, window=(99, 0), sinks=3, dtype=ty)
+        clean = layer.decode(q, k, v, lens)
+        for t in (k, v):
+            t[0, 3:n - 100], t[:, n:] = float("nan"), float("inf")
+        assert torch.equal(layer.decode(q, k, v, lens), clean)
+
+
+def test_decode_past_32_bits():
+    """A cache of more than 2^32 elements: the rows of the last sequence lie past every 32-bit offset."""
+    ttc = _ttc()
+    b, cap, hk, d = 3, 1 << 20, 16, 128
+    k, v = (torch.zeros((b, cap, hk * d), dtype=BF16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(b, hk * d, generator=g).to(BF16).cuda()
+    n, left = cap - 1, 149
+    rows = slice(n - 1 - left, n)
+    k[2, rows], v[2, rows] = (torch.randn(left + 1, hk * d, generator=g).to(BF16).cuda() for _ in range(2))
+    o = ttc.WindowAttention(hk, d, window=(left, 0), dtype=BF16).decode(q, k, v, torch.tensor([n] * b, dtype=torch.int32).cuda())
+    m = torch.ones((1, left + 1), dtype=torch.bool, device="cuda")
+    qi = q[2].view(1, hk, d)
+    (y, bound), *_ = _reference(qi, k[2, rows].view(-1, hk, d), v[2, rows].view(-1, hk, d), qi, m, d ** -0.5, 2.0 ** -8, 1)
+    _close(o[2].view(1, hk, d), y, bound, "o")
+    assert not bool(o[:2].any())
+
+
+def test_sequences_past_32_bits():
+    """One sequence whose rows pass 2^32 bytes: its last queries and keys."""
+    ttc = _ttc()
+    n, h, d, last = (1 << 20) + 70, 16, 128, 300
+    q, k, v, do = (torch.zeros((n, h * d), dtype=BF16, device="cuda") for _ in range(4))
+    g = torch.Generator().manual_seed(3)
+    for t in (q, k, v, do):
+        t[-last:] = torch.randn(last, h * d, generator=g).to(BF16).cuda()
+    layer = ttc.WindowAttention(h, d, window=(20, 20), dtype=BF16)
+    o, saved = layer.forward(q, k, v)
+    grads = layer.backward(q, k, v, o, do, saved)
+    m = _seen(last, last, 20, 20, 0, "cuda")
+    cut = lambda t: t[-last:].view(last, h, d)  # noqa: E731
+    for name, x, (y, bound) in zip(("o", "dq", "dk", "dv"), (o,) + grads, _reference(*map(cut, (q, k, v, do)), m, d ** -0.5, 2.0 ** -8, 1)):
+        _close(cut(x)[40:], y[40:], bound[40:], name)  # the first 40 also see rows before the slice
+
+
+def test_wrong_offsets_stay_inside():
+    """Offsets past the end or out of order are cut: the rows beside the buffers keep their values."""
+    ttc = _ttc()
+    n, w = 200, 2 * 64
+    whole = torch.full((n + 512, w), 7.0, dtype=BF16, device="cuda")
+    o = whole[256:256 + n]
+    q, k, v, do = _inputs([n], [n], 2, 2, 64, BF16, 5)
+    layer = ttc.WindowAttention(2, 64, window=(30, 30), dtype=BF16)
+    for off in ([0, 150, 900], [-40, 100, 200], [0, 150, 90], [300, 400, 500]):
+        t = torch.tensor(off, dtype=torch.int32).cuda()
+        layer.forward(q, k, v, batch=2, q_offsets=t, k_offsets=t, out=o)
+        torch.cuda.synchronize()
+        assert bool((whole[:256] == 7).all()) and bool((whole[256 + n:] == 7).all())
+
+
+def test_nothing_to_do():
+    ttc = _ttc()
+    layer = ttc.WindowAttention(2, 64, dtype=BF16)
+    none, some = torch.empty((0, 128), dtype=BF16, device="cuda"), torch.randn(5, 128, device="cuda").to(BF16)
+    o, saved = layer.forward(none, some, some)
+    dq, dk, dv = layer.backward(none, some, some, o, none, saved)
+    assert o.shape == dq.shape == (0, 128) and not bool(dk.any()) and not bool(dv.any())
+    o, saved = layer.forward(some, none, none)
+    dq, dk, dv = layer.backward(some, none, none, o, some, saved)
+    assert not bool(o.any()) and not bool(dq.any()) and dk.shape == (0, 128)
+    assert layer.decode(none, torch.empty((0, 8, 128), dtype=BF16, device="cuda"), torch.empty((0, 8, 128), dtype=BF16, device="cuda"),
+                        torch.empty(0, dtype=torch.int32, device="cuda")).shape == (0, 128)
+
+
+@pytest.mark.parametrize("n,ragged", [(500, False), (90, True), (700, True)])
+def test_repeatable_and_captured(n, ragged):
+    """Bitwise the same on every call, and in a graph replayed between eager work."""
+    ttc = _ttc()
+    lens = [n, n // 3, n // 2] if ragged else [n, n, n]
+    q, k, v, do = _inputs(lens, lens, 4, 2, 64, BF16, 6)
+    layer = ttc.WindowAttention(4, 64, 2, window=(100, 100), sinks=2, dtype=BF16)
+    off = _offsets(lens) if ragged else None
+    kw = dict(batch=3, q_offsets=off, k_offsets=off, max_q=n)
+    caches = [torch.randn(3, 900, 128, device="cuda").to(BF16) for _ in range(2)]
+    rows = torch.tensor([900, 3, 500], dtype=torch.int32).cuda()
+
+    def step():
+        o, saved = layer.forward(q, k, v, **kw)
+        return (o,) + layer.backward(q, k, v, o, do, saved, **kw) + (layer.decode(q[:3], *caches, rows),)
+
+    first = [t.clone() for t in step()]
+    assert all(torch.equal(a, b) for a, b in zip(first, step()))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    q0 = q.clone()
+    for i in range(4):
+        q.copy_(q0 * (1 + i))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step())), i
+
+
+def test_other_stream():
+    ttc = _ttc()
+    q, k, v, do = _inputs([300], [300], 2, 2, 64, BF16, 7)
+    layer = ttc.WindowAttention(2, 64, window=(40, 40), dtype=BF16)
+
+    def step():
+        o, saved = layer.forward(q, k, v)
+        return (o,) + layer.backward(q, k, v, o, do, saved)
+
+    want = step()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = step()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals():
+    ttc = _ttc()
+    layer = ttc.WindowAttention(4, 64, 2, dtype=BF16)
+    z = lambda *s, t=BF16: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    q, kv = z(6, 256), z(6, 128)
+    off = torch.tensor([0, 2, 6], dtype=torch.int32).cuda()
+    for call in (lambda: layer.forward(z(6, 128), kv, kv), lambda: layer.forward(q, kv, z(5, 128)), lambda: layer.forward(q, z(6, 128, t=F32), kv),
+                 lambda: layer.forward(z(256, 6).t(), kv, kv), lambda: layer.forward(q, kv, kv, batch=2, q_offsets=off),
+                 lambda: layer.forward(q, kv, kv, batch=3, q_offsets=off, k_offsets=off),
+                 lambda: layer.forward(q, kv, kv, batch=2, q_offsets=off.long(), k_offsets=off.long()),
+                 lambda: layer.decode(q, z(6, 9, 128), z(6, 8, 128), off), lambda: layer.decode(q, z(6, 9, 128), z(6, 9, 128), off),
+                 lambda: layer.forward(q, kv, kv, out=z(6, 256, t=F32)), lambda: ttc.WindowAttention(4, 64, dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ttc.TTCError) as e:  # sequences of one length that the rows do not make
+        layer.forward(q, kv, kv, batch=4)
+    assert e.value.code == 2
+    with pytest.raises(ttc.TTCError) as e:
+        layer.forward(z(2000)[4:1540].view(6, 256), kv, kv)
+    assert e.value.code == 5
+    with pytest.raises(ttc.TTCError) as e:
+        layer.forward(z(60, 256), z(60, 128), z(60, 128), saved=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 6
