@@ -156,6 +156,58 @@ ttc_status ttc_attn_decode(const ttc_attn_desc* desc, int64_t batch,
                            void* scratch, size_t scratch_bytes,
                            ttc_stream_t stream);
 
+/* ---- orthogonalised update of the cores ----------------------------------- */
+
+/* A matrix to update: rows x cols fp32, row-major, contiguous; a core of shape
+ * (r0, n, r1) is the matrix (r0 n) x r1, say.  w, g, m - device pointers to the
+ * weight, its gradient and its momentum, 4-byte aligned.  The smaller side is at
+ * most TTC_ORTHO_MAX_SIDE (ranks are at most TTC_MAX_RANK). */
+typedef struct {
+  int64_t rows, cols;
+  float* w;
+  const float* g;
+  float* m;
+} ttc_ortho_mat;
+
+#define TTC_ORTHO_MAX_SIDE 128
+
+/* With the look-ahead (nesterov != 0):
+ *   m <- mu m + g,  u = g + mu m  (without: u = m),  X = u / max(|u|, eps),
+ *   `steps` times  X <- a X + b X A + c X A A,  A = X^T X,
+ *   w <- (1 - lr weight_decay) w - lr sqrt(max(1, rows / cols)) X
+ * with |u| the root of the sum of squares.  A matrix whose smaller side is its
+ * rows is taken by its transpose, which gives the same X. */
+typedef struct {
+  int32_t steps;    /* 1 .. 32              */
+  int32_t nesterov; /* look-ahead: 0 or 1   */
+  float a, b, c;    /* finite               */
+  float eps;        /* > 0                  */
+  float lr, mu, weight_decay;
+} ttc_ortho_desc;
+
+/* Bytes of the plan (the matrices as the kernel reads them) and of the step's
+ * scratch (matrices whose smaller side is over 64).  Host-only. */
+ttc_status ttc_ortho_workspace(int64_t n, const ttc_ortho_mat* mats,
+                               size_t* plan_bytes, size_t* scratch_bytes);
+
+/* Writes the plan of n matrices to `plan`, HOST memory; the caller copies it to
+ * the device.  It holds the matrices' addresses and sizes and stays valid as
+ * long as they do. */
+ttc_status ttc_ortho_plan(int64_t n, const ttc_ortho_mat* mats, void* plan,
+                          size_t plan_bytes);
+
+/*
+ * One step of all n matrices, which share no memory.
+ *   mats - HOST array, as given to ttc_ortho_plan;  plan - device copy of the
+ *   plan;  w and m are updated in place, g is read
+ * A matrix that holds a NaN or an infinity gives a NaN one and leaves the
+ * others alone.
+ */
+ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n,
+                          const ttc_ortho_mat* mats, const void* plan,
+                          size_t plan_bytes, void* scratch,
+                          size_t scratch_bytes, ttc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

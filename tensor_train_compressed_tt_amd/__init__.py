@@ -72,6 +72,9 @@ EXPORTS = [
     "ttc_attn_bwd",
     "ttc_attn_decode_workspace",
     "ttc_attn_decode",
+    "ttc_ortho_workspace",
+    "ttc_ortho_plan",
+    "ttc_ortho_step",
 ]
 
 
@@ -149,6 +152,30 @@ class AttnSeqs(ctypes.Structure):
     ]
 
 
+class OrthoMat(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("w", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+    ]
+
+
+class OrthoDesc(ctypes.Structure):
+    _fields_ = [
+        ("steps", ctypes.c_int32),
+        ("nesterov", ctypes.c_int32),
+        ("a", ctypes.c_float),
+        ("b", ctypes.c_float),
+        ("c", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("lr", ctypes.c_float),
+        ("mu", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -168,6 +195,8 @@ def lib() -> ctypes.CDLL:
     N = ctypes.POINTER(NormDesc)
     A = ctypes.POINTER(AttnDesc)
     S = ctypes.POINTER(AttnSeqs)
+    M = ctypes.POINTER(OrthoMat)
+    O = ctypes.POINTER(OrthoDesc)
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "tt_linear_workspace": [D, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
@@ -207,6 +236,9 @@ def lib() -> ctypes.CDLL:
         "ttc_attn_bwd": [A, S, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _SZ, _P],
         "ttc_attn_decode_workspace": [A, _I64, _I64, ctypes.POINTER(_SZ)],
         "ttc_attn_decode": [A, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P],
+        "ttc_ortho_workspace": [_I64, M, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+        "ttc_ortho_plan": [_I64, M, _P, _SZ],
+        "ttc_ortho_step": [O, _I64, M, _P, _SZ, _P, _SZ, _P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -545,6 +577,32 @@ def ttc_attn_decode(desc, batch, capacity, q, k, v, lens, o, scratch, scratch_by
     _check("ttc_attn_decode", code)
 
 
+def make_ortho_mats(mats):
+    """Host array of matrices: (rows, cols, w, g, m) each, device addresses."""
+    return (OrthoMat * len(mats))(*[OrthoMat(*m) for m in mats])
+
+
+def make_ortho_desc(lr, mu=0.95, weight_decay=0.0, nesterov=True, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7):
+    return OrthoDesc(int(steps), int(bool(nesterov)), *[float(x) for x in coeffs], float(eps), float(lr), float(mu),
+                     float(weight_decay))
+
+
+def ttc_ortho_workspace(mats):
+    p, c = _SZ(0), _SZ(0)
+    _check("ttc_ortho_workspace", lib().ttc_ortho_workspace(len(mats), mats, ctypes.byref(p), ctypes.byref(c)))
+    return p.value, c.value
+
+
+def ttc_ortho_plan(mats, plan, plan_bytes):
+    """plan: HOST address."""
+    _check("ttc_ortho_plan", lib().ttc_ortho_plan(len(mats), mats, plan, plan_bytes))
+
+
+def ttc_ortho_step(desc, mats, plan, plan_bytes, scratch, scratch_bytes, stream=0):
+    code = lib().ttc_ortho_step(ctypes.byref(desc), len(mats), mats, plan, plan_bytes, scratch, scratch_bytes, stream)
+    _check("ttc_ortho_step", code)
+
+
 def trace_start():
     _check("ttc_trace_start", lib().ttc_trace_start())
 
@@ -579,4 +637,4 @@ from .torch_api import (  # noqa: E402,F401
     rank_grads_batch,
     prepare_batch,
 )
-from .block_api import LayerNorm, WindowAttention  # noqa: E402,F401
+from .block_api import LayerNorm, OrthogonalUpdate, WindowAttention  # noqa: E402,F401

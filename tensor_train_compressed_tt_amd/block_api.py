@@ -11,6 +11,8 @@ from . import (
     make_attn_desc,
     make_attn_seqs,
     make_norm_desc,
+    make_ortho_desc,
+    make_ortho_mats,
     ttc_attn_bwd,
     ttc_attn_decode,
     ttc_attn_decode_workspace,
@@ -19,6 +21,9 @@ from . import (
     ttc_norm_bwd,
     ttc_norm_fwd,
     ttc_norm_workspace,
+    ttc_ortho_plan,
+    ttc_ortho_step,
+    ttc_ortho_workspace,
 )
 from .torch_api import _ACT, _nbytes, _need, _need_buf, _stream
 
@@ -199,3 +204,41 @@ class WindowAttention:
         ttc_attn_decode(self.desc, batch, capacity, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(),
                         out.data_ptr(), scratch.data_ptr(), _nbytes(scratch), _stream())
         return out
+
+
+class OrthogonalUpdate:
+    """The step of an optimiser that orthogonalises its update, for the cores of
+    a model: ``weights``, ``grads`` and ``momenta`` are lists of fp32 device
+    tensors of one shape each.  A tensor of two dimensions is a matrix as it is;
+    one of more, such as a core (r0, n, r1), is taken as the matrix whose columns
+    are its last dimension, or, if that is 1, whose rows are its first.
+
+    ``step`` reads the gradients and updates weights and momenta in place; the
+    tensors must stay where they are.
+    """
+
+    def __init__(self, weights, grads, momenta, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7):
+        if not len(weights) == len(grads) == len(momenta):
+            raise ValueError("weights, grads and momenta must be lists of one length")
+        self.tensors = list(weights), list(grads), list(momenta)
+        self.steps, self.coeffs, self.eps = int(steps), tuple(float(x) for x in coeffs), float(eps)
+        mats = []
+        for k, (w, g, m) in enumerate(zip(*self.tensors)):
+            _need(w, f"weights[{k}]", torch.float32)
+            _need(g, f"grads[{k}]", torch.float32, tuple(w.shape))
+            _need(m, f"momenta[{k}]", torch.float32, tuple(w.shape))
+            if w.dim() < 2:
+                raise ValueError(f"weights[{k}] has fewer than two dimensions")
+            cols = w.shape[-1] if w.dim() == 2 or w.shape[-1] > 1 else w.numel() // max(w.shape[0], 1)
+            mats.append((w.numel() // max(cols, 1), cols, w.data_ptr(), g.data_ptr(), m.data_ptr()))
+        self.mats = make_ortho_mats(mats)
+        pb, sb = ttc_ortho_workspace(self.mats)
+        host = torch.empty(max(pb, 16), dtype=torch.uint8)
+        ttc_ortho_plan(self.mats, host.data_ptr(), pb)
+        device = weights[0].device if weights else "cuda"
+        self.plan, self.scratch = host.to(device), _bytes(sb, device)
+
+    def step(self, lr, mu=0.95, weight_decay=0.0, nesterov=True):
+        desc = make_ortho_desc(lr, mu, weight_decay, nesterov, self.steps, self.coeffs, self.eps)
+        ttc_ortho_step(desc, self.mats, self.plan.data_ptr(), _nbytes(self.plan), self.scratch.data_ptr(),
+                       _nbytes(self.scratch), _stream())

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libttc.so")
 
 SOURCES = ["tt_plan.cpp", "ttc_trace.cpp", "tt_linear.hip", "ttm_embed.hip",
-           "ttc_norm.hip", "ttc_attn.hip"]
+           "ttc_norm.hip", "ttc_attn.hip", "ttc_ortho.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

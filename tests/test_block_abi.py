@@ -87,3 +87,31 @@ def test_attention_errors_before_launch():
     ttc.ttc_attn_fwd(d, ttc.make_attn_seqs(1, 0, 0), None, None, None, None, None, 0)  # no rows: nothing is touched
     ttc.ttc_attn_bwd(d, ttc.make_attn_seqs(1, 0, 0), None, None, None, None, None, None, 0, None, None, None, None, 0)
     ttc.ttc_attn_decode(d, 0, 64, None, None, None, None, None, None, 0)
+
+
+def test_ortho_matrices_and_sizes():
+    ok = (240, 30, 16, 16, 16)
+    mats = ttc.make_ortho_mats([ok, (100, 65, 4, 8, 12)])
+    pb, sb = ttc.ttc_ortho_workspace(mats)
+    assert pb % 2 == 0 and sb > 0 and ttc.ttc_ortho_workspace(ttc.make_ortho_mats([ok])) == (pb // 2, 0)
+    assert ttc.ttc_ortho_workspace(ttc.make_ortho_mats([])) == (0, 0)
+    for bad, code in (((0, 4, 16, 16, 16), 2), ((4, -1, 16, 16, 16), 2), ((129, 129, 16, 16, 16), 2), ((1 << 31, 4, 16, 16, 16), 2),
+                      ((4, 4, None, 16, 16), 1), ((4, 4, 16, None, 16), 1), ((4, 4, 16, 16, None), 1), ((4, 4, 18, 16, 16), 5)):
+        assert _code(ttc.ttc_ortho_workspace, ttc.make_ortho_mats([ok, bad])) == code, bad
+
+
+def test_ortho_errors_before_launch():
+    import ctypes
+    mats = ttc.make_ortho_mats([(240, 30, 16, 16, 16), (100, 65, 4, 8, 12)])
+    pb, sb = ttc.ttc_ortho_workspace(mats)
+    host = ctypes.create_string_buffer(pb)
+    ttc.ttc_ortho_plan(mats, ctypes.addressof(host), pb)
+    assert _code(ttc.ttc_ortho_plan, mats, None, pb) == 1 and _code(ttc.ttc_ortho_plan, mats, ctypes.addressof(host), pb - 1) == 6
+    step = dict(plan=16, plan_bytes=pb, scratch=16, scratch_bytes=sb)
+    call = lambda d={}, **kw: ttc.ttc_ortho_step(ttc.make_ortho_desc(**{"lr": 0.1, **d}), mats, **{**step, **kw})  # noqa: E731
+    assert _code(lambda: call(plan=None)) == 1 and _code(lambda: call(scratch=None)) == 1
+    assert _code(lambda: call(plan=8)) == 5 and _code(lambda: call(scratch=8)) == 5
+    assert _code(lambda: call(plan_bytes=pb - 1)) == 6 and _code(lambda: call(scratch_bytes=sb - 1)) == 6
+    for d in (dict(steps=0), dict(steps=33), dict(eps=0.0), dict(lr=float("nan")), dict(mu=float("inf")), dict(coeffs=(1.0, float("nan"), 0.0))):
+        assert _code(lambda: call(d)) == 2, d
+    ttc.ttc_ortho_step(ttc.make_ortho_desc(0.1), ttc.make_ortho_mats([]), None, 0, None, 0)

@@ -1,0 +1,205 @@
+"""GPU parity of the orthogonalised update against its formulas in 64 bits.
+
+Tolerances.  m is one fp32 operation or two: 2^-23 of |mu m| + |g|.  X is
+X_0 Q: X_0's elements carry three fp32 roundings (u, 1 / |u|, their product), Q
+one, and the product sums at most 128 terms in fp32.  With |Q| = a^n at most in
+norm (p is a at most on [0, 1], and a singular value near zero is multiplied by a
+each step), an error of e |X_0| = e in X_0 or Q comes out as e a^n in the norm of
+a row or less; 16 fp32 steps cover the roundings and the sum.  So an element of X
+is off by at most 16 2^-24 a^n, and by 2^-24 of itself where it is stored.  The
+same holds for the formula's own recurrence in fp32.  w adds two roundings of its
+terms.
+"""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+F32 = torch.float32
+E32 = 2.0 ** -24
+COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def _ttc():
+    import tensor_train_compressed_tt_amd as ttc
+    return ttc
+
+
+def _matrices(shapes, seed, rank=None, size=1e-3):
+    g = torch.Generator().manual_seed(seed)
+    out = []
+    for r, c in shapes:
+        t = [torch.randn(r, c, generator=g) * s for s in (0.15, size, 3 * size)]
+        if rank is not None:  # singular values that fall off to nothing
+            for k in (1, 2):
+                u = torch.randn(r, rank, generator=g) * torch.logspace(0, -6, rank)
+                t[k] = size * u @ torch.randn(rank, c, generator=g)
+        out.append([x.cuda() for x in t])
+    return out
+
+
+def _reference(w, g, m, lr, mu, wd, nesterov, steps, coeffs, eps):
+    w, g, m = (x.double().cpu() for x in (w, g, m))
+    f = lambda x: float(torch.tensor(x, dtype=F32))  # noqa: E731
+    lr, mu, wd, eps, a, b, c = map(f, (lr, mu, wd, eps, *coeffs))
+    m = mu * m + g
+    u = g + mu * m if nesterov else m
+    x = u / max(float(u.norm()), eps)
+    for _ in range(steps):
+        s = x.t() @ x if x.shape[0] >= x.shape[1] else x @ x.t()
+        p = b * s + c * s @ s
+        x = a * x + (x @ p if x.shape[0] >= x.shape[1] else p @ x)
+    scale = math.sqrt(max(1.0, w.shape[0] / w.shape[1]))
+    return m, x, (1 - lr * wd) * w - lr * scale * x, lr * scale
+
+
+def _check(shapes, seed=0, lr=0.02, mu=0.95, wd=0.01, nesterov=True, steps=5, coeffs=COEFFS, eps=1e-7, rank=None, size=1e-3):
+    ttc = _ttc()
+    mats = _matrices(shapes, seed, rank, size)
+    before = [[x.clone() for x in t] for t in mats]
+    upd = ttc.OrthogonalUpdate([t[0] for t in mats], [t[1] for t in mats], [t[2] for t in mats], steps=steps, coeffs=coeffs, eps=eps)
+    upd.step(lr, mu, wd, nesterov)
+    torch.cuda.synchronize()
+    for k, (t, old) in enumerate(zip(mats, before)):
+        m, x, w, rate = _reference(*old, lr, mu, wd, nesterov, steps, coeffs, eps)
+        assert torch.equal(t[1], old[1])
+        off = (t[2].double().cpu() - m).abs() - 2 * E32 * (mu * old[2].double().cpu().abs() + old[1].double().cpu().abs())
+        assert float(off.max()) <= 0, f"m of {shapes[k]}: {float(off.max()):.3g}"
+        bound = rate * (16 * E32 * abs(coeffs[0]) ** steps + E32 * x.abs()) + 3 * E32 * (old[0].double().cpu().abs() + rate * x.abs())
+        off = (t[0].double().cpu() - w).abs() - bound
+        assert float(off.max()) <= 0, f"w of {shapes[k]}: {float(off.max()):.3g} over its bound"
+
+
+SIDES = [1, 2, 3, 4, 7, 8, 15, 16, 17, 30, 31, 32, 33, 47, 48, 49, 63, 64, 65, 79, 96, 100, 127, 128]
+
+
+@pytest.mark.parametrize("side", SIDES)
+@pytest.mark.parametrize("length", [1, 3, 16, 100, 129, 517])
+def test_shapes(side, length):
+    _check([(length, side), (side, length)], seed=side * 1000 + length)
+
+
+def test_many_of_unequal_shapes():
+    """More work-groups than run at once, of every kind, in one launch."""
+    _check([(1 + (k * 37) % 300, 1 + (k * 11) % 128) for k in range(300)], seed=1)
+
+
+def test_cores_of_an_encoder():
+    d, f, r, shapes = (12, 8, 8), (12, 16, 16), 30, []
+    for modes in [d + d] * 4 + [f + d, d + f]:
+        for k, n in enumerate(modes):
+            r0, r1 = (1 if k == 0 else r), (1 if k == len(modes) - 1 else r)
+            shapes.append((r0 * n, r1) if r1 > 1 else (r0, n))
+    _check(shapes + [(32 * 12, 16), (16 * 32 * 8, 16), (16, 32 * 8)], seed=2)
+
+
+@pytest.mark.parametrize("rank", [1, 5, 30])
+def test_singular_values_that_fall_off(rank):
+    """A gradient of low rank: singular values down to 1e-6 of the largest and, past them, rounding."""
+    _check([(300, 48), (64, 64), (30, 30), (128, 500), (512, 64)], seed=rank, rank=rank, mu=0.0)
+
+
+@pytest.mark.parametrize("kw", [dict(nesterov=False), dict(mu=0.0), dict(wd=0.0), dict(steps=1), dict(steps=2), dict(steps=8, coeffs=(1.5, -0.5, 0.0)),
+                                dict(eps=10.0), dict(lr=0.0), dict(size=1e-25), dict(size=1e12)])
+def test_parameters(kw):
+    _check([(240, 30), (30, 8), (12, 30), (70, 70)], **kw)
+
+
+def test_zero_gradient_and_momentum():
+    ttc = _ttc()
+    w = torch.randn(60, 20).cuda()
+    was, g, m = w.clone(), torch.zeros(60, 20, device="cuda"), torch.zeros(60, 20, device="cuda")
+    ttc.OrthogonalUpdate([w], [g], [m]).step(0.5, weight_decay=0.25)
+    assert torch.equal(w, was * 0.875) and not bool(m.any())
+
+
+def test_pruned_columns_stay_untouched():
+    """Columns without gradient get no update, to the bit."""
+    ttc = _ttc()
+    (w, g, m), = _matrices([(240, 30)], 3)
+    dead = torch.arange(0, 30, 3, device="cuda")
+    g[:, dead], m[:, dead] = 0.0, 0.0
+    was = w.clone()
+    ttc.OrthogonalUpdate([w], [g], [m]).step(0.1)
+    assert torch.equal(w[:, dead], was[:, dead]) and not bool(m[:, dead].any()) and not torch.equal(w, was)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nan_and_infinity_stay_in_their_matrix(bad):
+    ttc = _ttc()
+    shapes = [(100, 20), (64, 64), (100, 20)]
+    runs = []
+    for plant in (False, True):
+        mats = _matrices(shapes, 4)
+        if plant:
+            mats[1][1][5, 5] = bad
+        ttc.OrthogonalUpdate(*[[t[k] for t in mats] for k in range(3)]).step(0.1)
+        runs.append([t[0] for t in mats])
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][2], runs[1][2])
+    assert bool(torch.isnan(runs[1][1]).all())
+
+
+def test_cores_of_three_dimensions():
+    ttc = _ttc()
+    for shape, mat in (((30, 8, 30), (240, 30)), ((30, 8, 1), (30, 8)), ((1, 12, 30), (12, 30)), ((16, 32, 8, 16), (4096, 16)), ((16, 32, 8, 1), (16, 256))):
+        a, b = _matrices([mat], 5), _matrices([mat], 5)
+        ttc.OrthogonalUpdate(*[[x.view(shape)] for x in a[0]]).step(0.1)
+        ttc.OrthogonalUpdate(*[[x] for x in b[0]]).step(0.1)
+        assert all(torch.equal(x, y) for x, y in zip(a[0], b[0])), shape
+
+
+def test_unaligned_matrices():
+    """Matrices that begin at any fourth byte."""
+    ttc = _ttc()
+    for at in (1, 2, 3):
+        a, b = _matrices([(60, 20)], 6), _matrices([(60, 20)], 6)
+        moved = []
+        for x in a[0]:
+            flat = torch.zeros(1200 + at + 5, device="cuda")
+            flat[at:at + 1200] = x.view(-1)
+            moved.append(flat)
+        ttc.OrthogonalUpdate(*[[f[at:at + 1200].view(60, 20)] for f in moved]).step(0.1)
+        ttc.OrthogonalUpdate(*[[x] for x in b[0]]).step(0.1)
+        for f, y in zip(moved, b[0]):
+            torch.testing.assert_close(f[at:at + 1200].view(60, 20), y, rtol=1e-5, atol=1e-6)
+            assert not bool(f[:at].any()) and not bool(f[at + 1200:].any())
+
+
+def test_repeatable_and_captured():
+    ttc = _ttc()
+    shapes = [(240, 30), (512, 64), (100, 100), (30, 8)]
+    a, b, c = (_matrices(shapes, 7) for _ in range(3))
+    upd = [ttc.OrthogonalUpdate(*[[t[k] for t in x] for k in range(3)]) for x in (a, b, c)]
+    for u in upd[:2]:
+        for _ in range(4):
+            u.step(0.1)
+    torch.cuda.synchronize()
+    same = lambda x, y: all(torch.equal(p, q) for s, t in zip(x, y) for p, q in zip(s, t))  # noqa: E731
+    assert same(a, b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        upd[2].step(0.1)
+    for k in range(4):
+        g.replay()
+        torch.cuda.synchronize()
+        upd[0].step(0.1)  # eager work between the replays
+    assert same(b, c)
+
+
+def test_refusals():
+    ttc = _ttc()
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    for args in (([z(4, 4)], [z(4, 4)], []), ([z(4, 4)], [z(4, 5)], [z(4, 4)]), ([z(4)], [z(4)], [z(4)]),
+                 ([z(4, 4).double()], [z(4, 4).double()], [z(4, 4).double()]), ([z(4, 6).t()], [z(6, 4)], [z(6, 4)])):
+        with pytest.raises(ValueError):
+            ttc.OrthogonalUpdate(*args)
+    with pytest.raises(ttc.TTCError) as e:
+        ttc.OrthogonalUpdate([z(129, 129)], [z(129, 129)], [z(129, 129)])
+    assert e.value.code == 2
+    with pytest.raises(ttc.TTCError) as e:
+        ttc.OrthogonalUpdate([z(4, 4)], [z(4, 4)], [z(4, 4)], steps=0).step(0.1)
+    assert e.value.code == 2
+    ttc.OrthogonalUpdate([], [], []).step(0.1)
