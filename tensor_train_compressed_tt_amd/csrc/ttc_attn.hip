@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/ttc_block.h"
 #include "ttc_device.hpp"
 #include "ttc_trace.hpp"
@@ -176,8 +178,8 @@ __device__ void row_dkv(const AttnArgs& a, const typename Elem<T>::type* q, cons
     float ds = 0.f, e = 0.f;
     if (lane < n) {
       const int64_t i = i0 + lane;
-      e = exp2f(a.scale2 * dot_row<T>(q + i * ldq, k, a.dim) - lse[i * a.heads]);
-      ds = e * (dot_row<T>(d_o + i * ldq, v, a.dim) - delta[i * a.heads]) * a.scale;
+      e = exp2f(a.scale2 * dot_row<T>(q + i * ldq, k, a.dim) - lse[i]);
+      ds = e * (dot_row<T>(d_o + i * ldq, v, a.dim) - delta[i]) * a.scale;
     }
     for (int i = 0; i < n; ++i) {
       const float ws = lane_value(ds, i), we = lane_value(e, i);
@@ -194,82 +196,618 @@ __device__ void row_dkv(const AttnArgs& a, const typename Elem<T>::type* q, cons
   }
 }
 
-// work-group -> (tile, head of `heads`, sequence); the tiles of one head follow each other
+// ---- tiles ---------------------------------------------------------------------
+//
+// A wave holds 32 rows of one side as columns of the 32 x 32 matrix products
+// (lane l: column l % 32) and meets tiles of 64 rows of the other side in LDS:
+//   forward, dq:  columns are queries, S^T = K Q^T, dP^T = V dO^T
+//   dk and dv:    columns are keys,    S = Q K^T,   dP = dO V^T
+// A lane then has 16 scores of its own column: a softmax's maximum and sum are
+// in-lane but for one exchange between the wave's halves, and what goes into
+// the next product (P, dS) is its right operand as it lies in the registers,
+// since the left operand's rows can be read in the order that they came in.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kTile = 64;          // rows of a tile in LDS
+constexpr int kOwn = 32;           // rows of a wave
+constexpr int kBlock = kOwn * (kThreads / 64);
+
+// 32 x 32 products: a lane gives 16 bytes of row l % 32 of A and of column
+// l % 32 of B, those of k-group l / 32; element i of the result is row
+// 8 (i / 4) + 4 (l / 32) + i % 4 of column l % 32.
+template <typename T>
+struct Mma32;
+template <>
+struct Mma32<bf16_t> {
+  static constexpr int KSTEP = 16;
+  __device__ __forceinline__ static f32x16 mma(u16x8 a, u16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+};
+template <>
+struct Mma32<float> {
+  static constexpr int KSTEP = 8;
+  __device__ __forceinline__ static f32x16 mma(f32x4 a, f32x4 b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+};
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// NS: the head's elements in tiles of 32
+template <typename T, int NS>
+struct Geo {
+  typedef typename Elem<T>::type E;
+  static constexpr int DP = 32 * NS;
+  static constexpr int EPV = 16 / (int)sizeof(E);
+  static constexpr int LD = DP + EPV;                 // 16 bytes more: rows start in other banks
+  static constexpr int KF = DP / Mma32<T>::KSTEP;     // k-steps over the head's elements
+  static constexpr int KP = kTile / 2 / Mma32<T>::KSTEP;  // k-steps over 32 rows of a tile
+  static constexpr int CPR = DP / EPV;                // 16-byte pieces of a row
+  static constexpr int NL = kTile * CPR / kThreads;   // pieces that a thread brings
+};
+
+// a thread's share of a tile on its way from memory to LDS
+template <typename T, int NS>
+struct Pieces {
+  typedef Geo<T, NS> G;
+  typename Mma<T>::frag f[G::NL];
+  // rows [0, rows) of ldb bytes each, the first dim elements of a row; zeros beyond
+  __device__ __forceinline__ void load(const typename G::E* base, int rows, int ldb, int dim) {
+    rows = min(rows, kTile);
+    const rsrc_t r = make_rsrc(base, rows < 1 ? 0 : (int64_t)(rows - 1) * ldb + dim * (int)sizeof(typename G::E));
+#pragma unroll
+    for (int n = 0; n < G::NL; ++n) {
+      const int x = threadIdx.x + n * kThreads, row = x / G::CPR, c = x - row * G::CPR;
+      f[n] = buf_frag<T>(r, row < rows && c * G::EPV < dim ? (uint32_t)(row * ldb + c * 16) : kNoOff);
+    }
+  }
+  __device__ __forceinline__ void store(typename G::E* tile) const {
+#pragma unroll
+    for (int n = 0; n < G::NL; ++n) {
+      const int x = threadIdx.x + n * kThreads, row = x / G::CPR, c = x - row * G::CPR;
+      *reinterpret_cast<typename Mma<T>::frag*>(tile + row * G::LD + c * G::EPV) = f[n];
+    }
+  }
+};
+
+// the wave's own 32 rows as the right operand (row: this lane's, or none)
+template <typename T, int NS>
+struct Own {
+  typedef Geo<T, NS> G;
+  typename Mma<T>::frag f[G::KF];
+  __device__ __forceinline__ void load(const typename G::E* base, int rows, int ldb, int dim) {
+    const int c = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
+    rows = min(rows, kOwn);
+    const rsrc_t r = make_rsrc(base, rows < 1 ? 0 : (int64_t)(rows - 1) * ldb + dim * (int)sizeof(typename G::E));
+#pragma unroll
+    for (int k = 0; k < G::KF; ++k) {
+      const int d = k * Mma32<T>::KSTEP + g * G::EPV;
+      f[k] = buf_frag<T>(r, c < rows && d < dim ? (uint32_t)(c * ldb + d * (int)sizeof(typename G::E)) : kNoOff);
+    }
+  }
+  __device__ __forceinline__ void negate() {
+#pragma unroll
+    for (int k = 0; k < G::KF; ++k)
+#pragma unroll
+      for (int e = 0; e < G::EPV; ++e) {
+        if constexpr (sizeof(typename G::E) == 2)
+          f[k][e] ^= 0x8000;
+        else
+          f[k][e] = -f[k][e];
+      }
+  }
+};
+
+// rows [32 half, 32 half + 32) of a tile times the wave's own rows
+template <typename T, int NS>
+__device__ __forceinline__ f32x16 rows_times_own(const typename Elem<T>::type* tile, int half, const Own<T, NS>& own) {
+  typedef Geo<T, NS> G;
+  const typename G::E* p = tile + (32 * half + (threadIdx.x & 31)) * G::LD + ((threadIdx.x >> 5) & 1) * G::EPV;
+  f32x16 c = zero16();
+#pragma unroll
+  for (int k = 0; k < G::KF; ++k) c = Mma32<T>::mma(lds_frag<T>(p + k * Mma32<T>::KSTEP), own.f[k], c);
+  return c;
+}
+
+// Left operand from the columns [32 dt, 32 dt + 32) of a tile: the rows that
+// hold, in result order, the values of k-step s of its half.  bf16: rows 0..3
+// and 8..11 (lanes 0..31) or 4..7 and 12..15 of a 16-row step, by the
+// transposing LDS read (lane 4 j + q of a block of 16 reads row j at columns
+// 4 q .. 4 q + 3, lane i gets column i).
+template <typename T, int NS>
+__device__ __forceinline__ typename Mma<T>::frag col_frag(const typename Elem<T>::type* tile, int half, int s, int dt) {
+  typedef Geo<T, NS> G;
+  const int l = threadIdx.x & 63;
+  if constexpr (sizeof(typename G::E) == 2) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const int i = l & 15, blk = l >> 4;
+    const typename G::E* p =
+        tile + (32 * half + 16 * s + 4 * (blk >> 1) + (i >> 2)) * G::LD + 32 * dt + 16 * (blk & 1) + 4 * (i & 3);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * G::LD));
+    return __builtin_bit_cast(u16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    const typename G::E* p = tile + (32 * half + 8 * s + 4 * (l >> 5)) * G::LD + 32 * dt + (l & 31);
+    return f32x4{p[0], p[G::LD], p[2 * G::LD], p[3 * G::LD]};
+  }
+}
+
+// right operand of k-step s from a result; bf16: rounded to nearest even, half a
+// step of 2^-8 of each P or dS, as they enter a bf16 product (sums stay fp32)
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::frag result_frag(const f32x16& c, int s) {
+  if constexpr (sizeof(typename Elem<T>::type) == 2) {
+    u32x4v w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = f32x2_to_bf16x2(c[8 * s + 2 * e], c[8 * s + 2 * e + 1]);
+    return __builtin_bit_cast(u16x8, w);
+  } else {
+    return f32x4{c[4 * s], c[4 * s + 1], c[4 * s + 2], c[4 * s + 3]};
+  }
+}
+
+// acc[dt] (columns of the tile x own rows) += tile^T c over the half's 32 rows
+template <typename T, int NS>
+__device__ __forceinline__ void cols_times_result(const typename Elem<T>::type* tile, int half, const f32x16& c,
+                                                  f32x16 (&acc)[NS]) {
+#pragma unroll
+  for (int s = 0; s < Geo<T, NS>::KP; ++s) {
+    const typename Mma<T>::frag b = result_frag<T>(c, s);
+#pragma unroll
+    for (int dt = 0; dt < NS; ++dt) acc[dt] = Mma32<T>::mma(col_frag<T, NS>(tile, half, s, dt), b, acc[dt]);
+  }
+}
+
+// acc[dt] times f to row `row` (this lane's; none where !on), four elements a store
+template <typename T, int NS>
+__device__ __forceinline__ void store_own(typename Elem<T>::type* row, bool on, const f32x16 (&acc)[NS], float f,
+                                          int dim) {
+  const int g = (threadIdx.x >> 5) & 1;
+#pragma unroll
+  for (int dt = 0; dt < NS; ++dt)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int d = 32 * dt + 8 * k + 4 * g;
+      if (!on || d >= dim) continue;
+      const float v[4] = {acc[dt][4 * k] * f, acc[dt][4 * k + 1] * f, acc[dt][4 * k + 2] * f, acc[dt][4 * k + 3] * f};
+      if constexpr (sizeof(typename Elem<T>::type) == 2)
+        *reinterpret_cast<uint2*>(row + d) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+      else
+        *reinterpret_cast<float4*>(row + d) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// Own rows whose sums hold a NaN, as bits.  A weight of zero times a value that
+// the row does not see, but others of the tile do, is a NaN where that value is
+// a NaN or an infinity; such rows are computed again one at a time.
+template <int NS>
+__device__ __forceinline__ uint32_t nan_rows(const f32x16 (&acc)[NS]) {
+  bool bad = false;
+#pragma unroll
+  for (int dt = 0; dt < NS; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bad |= acc[dt][i] != acc[dt][i];
+  const uint64_t b = __ballot(bad);
+  return (uint32_t)b | (uint32_t)(b >> 32);
+}
+
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// work-group -> (tile, head of `heads`, sequence).  The tiles of one head
+// follow each other on one of the eight dies (work-groups go to them in turn),
+// so that its keys stay in that die's cache.
 struct Place {
   int tile, head, b;
 };
 __device__ __forceinline__ Place place_of(const AttnArgs& a, int heads) {
-  const int g = blockIdx.x, r = g / a.tiles;
+  const int n = gridDim.x, x = blockIdx.x & 7, y = blockIdx.x >> 3, per = n >> 3, more = n & 7;
+  const int g = x * per + min(x, more) + y, r = g / a.tiles;
   return {g - r * a.tiles, r % heads, r / heads};
 }
 
-constexpr int kRows = kThreads / 64;
+// The tiles that queries at places p0 .. p1 see: [0, s) and [lo, hi).
+struct Tiles {
+  int s, lo, hi;
+  __device__ __forceinline__ int first() const { return s > 0 ? 0 : lo; }
+  __device__ __forceinline__ int after(int x) const { return x + 1 >= s && x + 1 < lo ? lo : x + 1; }
+};
+__device__ __forceinline__ Tiles key_tiles(const AttnArgs& a, int p0, int p1, int lk) {
+  const int end = min(lk, p1 + a.right + 1), lo = max(0, p0 - a.left);
+  Tiles t;
+  t.s = max(0, (min(min(a.sinks, lo), end) + kTile - 1) / kTile);
+  t.lo = end > lo ? lo / kTile : t.s;
+  t.hi = end > lo ? (end + kTile - 1) / kTile : t.s;
+  return t;
+}
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
-  typedef typename Elem<T>::type E;
+// of keys [j, j + n) by queries at places [p0, p1]: none seen, or all
+__device__ __forceinline__ bool none_seen(const AttnArgs& a, int j, int n, int p0, int p1, int lk) {
+  return j >= lk || j > p1 + a.right || (j + n - 1 < p0 - a.left && j >= a.sinks);
+}
+__device__ __forceinline__ bool all_seen(const AttnArgs& a, int j, int n, int p0, int p1, int lk) {
+  return j + n <= lk && j + n - 1 <= p0 + a.right && (j >= p1 - a.left || j + n <= a.sinks);
+}
+__device__ __forceinline__ bool seen(const AttnArgs& a, int j, int p, int lk) {
+  return j < lk && j <= p + a.right && (j >= p - a.left || j < a.sinks);
+}
+
+constexpr float kSlack = 8.f;  // P stays below 2^8 times its largest: far from overflow in fp32 and bf16
+
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(AttnArgs a) {
+  typedef Geo<T, NS> G;
+  typedef typename G::E E;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  E* const tiles = reinterpret_cast<E*>(lds_raw);
+  constexpr int TS = kTile * G::LD;
   const Place w = place_of(a, a.heads);
   const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
-  const int hk = w.head / (a.heads / a.kv_heads);
+  const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
+  const int hk = w.head / (a.heads / a.kv_heads), lk = sk.len, shift = sk.len - sq.len;
   const E* k = static_cast<const E*>(a.k) + sk.start * ldk + (int64_t)hk * a.dim;
   const E* v = static_cast<const E*>(a.v) + sk.start * ldk + (int64_t)hk * a.dim;
-  for (int64_t t = w.tile; t * kRows < sq.len; t += a.tiles) {
-    const int i = (int)t * kRows + threadIdx.x / 64;
-    if (i >= sq.len) continue;
-    const int64_t at = (sq.start + i) * ldq + (int64_t)w.head * a.dim;
-    float acc[2], lse;
-    row_fwd<T>(a, static_cast<const E*>(a.q) + at, k, v, ldk, i + sk.len - sq.len, sk.len, acc, lse);
-    row_store<T>(static_cast<E*>(a.o) + at, acc, a.dim);
-    if ((threadIdx.x & 63) == 0) a.lse[(sq.start + i) * a.heads + w.head] = lse;
+  const E* q = static_cast<const E*>(a.q) + sq.start * ldq + (int64_t)w.head * a.dim;
+  E* o = static_cast<E*>(a.o) + sq.start * ldq + (int64_t)w.head * a.dim;
+  float* lse = a.lse + (int64_t)w.head * a.tq + sq.start;
+  const int c = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float scale2 = fabsf(a.scale2);
+  for (int64_t t = w.tile; t * kBlock < sq.len; t += a.tiles) {
+    const int b0 = (int)t * kBlock, q0 = b0 + kOwn * wave, rows = min(sq.len - q0, kOwn);
+    const Tiles kt = key_tiles(a, b0 + shift, min(b0 + kBlock, sq.len) - 1 + shift, lk);
+    const int p0 = q0 + shift, p1 = p0 + rows - 1, p = p0 + c;
+    Own<T, NS> qf;
+    qf.load(q + (int64_t)q0 * ldq, rows, lbq, a.dim);
+    if (a.scale2 < 0.f) qf.negate();
+    f32x16 acc[NS];
+#pragma unroll
+    for (int dt = 0; dt < NS; ++dt) acc[dt] = zero16();
+    float m = -INFINITY, l = 0.f;
+    Pieces<T, NS> pk, pv;
+    int x = kt.first(), cur = 0;
+    __syncthreads();  // the last tile's readers are done
+    if (x < kt.hi) {
+      pk.load(k + (int64_t)x * kTile * ldk, lk - x * kTile, lbk, a.dim);
+      pv.load(v + (int64_t)x * kTile * ldk, lk - x * kTile, lbk, a.dim);
+      pk.store(tiles);
+      pv.store(tiles + TS);
+    }
+    while (x < kt.hi) {
+      const int nx = kt.after(x), j0 = x * kTile;
+      lds_barrier();
+      if (nx < kt.hi) {
+        pk.load(k + (int64_t)nx * kTile * ldk, lk - nx * kTile, lbk, a.dim);
+        pv.load(v + (int64_t)nx * kTile * ldk, lk - nx * kTile, lbk, a.dim);
+      }
+      const E *tk = tiles + cur * 2 * TS, *tv = tk + TS;
+      if (rows > 0 && !none_seen(a, j0, kTile, p0, p1, lk)) {
+        f32x16 s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = rows_times_own<T, NS>(tk, h, qf);
+        if (!all_seen(a, j0, kTile, p0, p1, lk)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              s[h][i] = seen(a, j0 + 32 * h + 8 * (i / 4) + 4 * g + i % 4, p, lk) ? s[h][i] : -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
+        top = max_halves(top) * scale2;
+        // the sums keep the maximum that they were begun with until a score
+        // passes it by far: any subtrahend gives the same quotient
+        if (__ballot(top > m + kSlack) != 0) {
+          const float mn = fmaxf(m, top);
+          const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+          m = mn;
+          l *= keep;
+#pragma unroll
+          for (int dt = 0; dt < NS; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] *= keep;
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], scale2, -sub));
+            l += s[h][i];
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) cols_times_result<T, NS>(tv, h, s[h], acc);
+      }
+      if (nx < kt.hi) {
+        cur ^= 1;
+        pk.store(tiles + cur * 2 * TS);
+        pv.store(tiles + cur * 2 * TS + TS);
+      }
+      x = nx;
+    }
+    l = sum_halves(l);
+    const uint32_t bad = rows > 0 ? nan_rows(acc) & (rows < 32 ? (1u << rows) - 1 : ~0u) : 0;
+    const bool on = c < rows && !((bad >> c) & 1);
+    store_own<T, NS>(o + (int64_t)(q0 + c) * ldq, on, acc, l == 0.f ? 0.f : 1.f / l, a.dim);
+    // a row that sees nothing weighs nothing in the backward
+    if (on && g == 0) lse[q0 + c] = l == 0.f ? INFINITY : m + __builtin_amdgcn_logf(l);
+    for (uint32_t left = bad; left; left &= left - 1) {
+      const int i = q0 + __builtin_ctz(left);
+      float r[2], stat;
+      row_fwd<T>(a, q + (int64_t)i * ldq, k, v, ldk, i + shift, lk, r, stat);
+      row_store<T>(o + (int64_t)i * ldq, r, a.dim);
+      if ((threadIdx.x & 63) == 0) lse[i] = stat;
+    }
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attn_dq(AttnArgs a) {
-  typedef typename Elem<T>::type E;
+// dq, and delta for k_attn_dkv
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads, 2) void k_attn_dq(AttnArgs a) {
+  typedef Geo<T, NS> G;
+  typedef typename G::E E;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  E* const tiles = reinterpret_cast<E*>(lds_raw);
+  constexpr int TS = kTile * G::LD;
   const Place w = place_of(a, a.heads);
   const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
-  const int hk = w.head / (a.heads / a.kv_heads), lane = threadIdx.x & 63;
+  const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
+  const int hk = w.head / (a.heads / a.kv_heads), lk = sk.len, shift = sk.len - sq.len;
   const E* k = static_cast<const E*>(a.k) + sk.start * ldk + (int64_t)hk * a.dim;
   const E* v = static_cast<const E*>(a.v) + sk.start * ldk + (int64_t)hk * a.dim;
-  for (int64_t t = w.tile; t * kRows < sq.len; t += a.tiles) {
-    const int i = (int)t * kRows + threadIdx.x / 64;
-    if (i >= sq.len) continue;
-    const int64_t at = (sq.start + i) * ldq + (int64_t)w.head * a.dim;
-    const E *d_o = static_cast<const E*>(a.d_o) + at, *o = static_cast<const E*>(a.o_in) + at;
-    float s = 0.f;
-    for (int c = lane; c < a.dim; c += 64) s += elem_to_f32<T>(d_o[c]) * elem_to_f32<T>(o[c]);
-    const float delta = wave_sum(s);
-    const int64_t st = (sq.start + i) * a.heads + w.head;
-    float acc[2];
-    row_dq<T>(a, static_cast<const E*>(a.q) + at, d_o, k, v, ldk, i + sk.len - sq.len, sk.len, a.lse[st], delta, acc);
-    row_store<T>(static_cast<E*>(a.dq) + at, acc, a.dim);
-    if (lane == 0) a.delta[st] = delta;
+  const int64_t head = sq.start * ldq + (int64_t)w.head * a.dim;
+  const E *q = static_cast<const E*>(a.q) + head, *o = static_cast<const E*>(a.o_in) + head;
+  const E* d_o = static_cast<const E*>(a.d_o) + head;
+  E* dq = static_cast<E*>(a.dq) + head;
+  const float* lse = a.lse + (int64_t)w.head * a.tq + sq.start;
+  float* delta = a.delta + (int64_t)w.head * a.tq + sq.start;
+  const int c = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float scale2 = fabsf(a.scale2);
+  for (int64_t t = w.tile; t * kBlock < sq.len; t += a.tiles) {
+    const int b0 = (int)t * kBlock, q0 = b0 + kOwn * wave, rows = min(sq.len - q0, kOwn);
+    const Tiles kt = key_tiles(a, b0 + shift, min(b0 + kBlock, sq.len) - 1 + shift, lk);
+    const int p0 = q0 + shift, p1 = p0 + rows - 1, p = p0 + c;
+    Own<T, NS> qf, of;
+    of.load(o + (int64_t)q0 * ldq, rows, lbq, a.dim);
+    qf.load(d_o + (int64_t)q0 * ldq, rows, lbq, a.dim);
+    float dl = 0.f;
+#pragma unroll
+    for (int f = 0; f < G::KF; ++f)
+#pragma unroll
+      for (int e = 0; e < G::EPV; ++e) dl += elem_to_f32<T>(of.f[f][e]) * elem_to_f32<T>(qf.f[f][e]);
+    dl = sum_halves(dl);
+    if (c < rows && g == 0) delta[q0 + c] = dl;
+    of = qf;  // dO
+    qf.load(q + (int64_t)q0 * ldq, rows, lbq, a.dim);
+    if (a.scale2 < 0.f) qf.negate();
+    const float sub = c < rows ? lse[q0 + c] : INFINITY;
+    f32x16 acc[NS];
+#pragma unroll
+    for (int dt = 0; dt < NS; ++dt) acc[dt] = zero16();
+    Pieces<T, NS> pk, pv;
+    int x = kt.first(), cur = 0;
+    __syncthreads();  // the last tile's readers are done
+    if (x < kt.hi) {
+      pk.load(k + (int64_t)x * kTile * ldk, lk - x * kTile, lbk, a.dim);
+      pv.load(v + (int64_t)x * kTile * ldk, lk - x * kTile, lbk, a.dim);
+      pk.store(tiles);
+      pv.store(tiles + TS);
+    }
+    while (x < kt.hi) {
+      const int nx = kt.after(x), j0 = x * kTile;
+      lds_barrier();
+      if (nx < kt.hi) {
+        pk.load(k + (int64_t)nx * kTile * ldk, lk - nx * kTile, lbk, a.dim);
+        pv.load(v + (int64_t)nx * kTile * ldk, lk - nx * kTile, lbk, a.dim);
+      }
+      const E *tk = tiles + cur * 2 * TS, *tv = tk + TS;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = j0 + 32 * h;
+        if (rows <= 0 || none_seen(a, j, 32, p0, p1, lk)) continue;
+        f32x16 s = rows_times_own<T, NS>(tk, h, qf);
+        const f32x16 dp = rows_times_own<T, NS>(tv, h, of);
+        if (all_seen(a, j, 32, p0, p1, lk)) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * (dp[i] - dl);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[i] = seen(a, j + 8 * (i / 4) + 4 * g + i % 4, p, lk)
+                       ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * (dp[i] - dl)
+                       : 0.f;
+        }
+        cols_times_result<T, NS>(tk, h, s, acc);
+      }
+      if (nx < kt.hi) {
+        cur ^= 1;
+        pk.store(tiles + cur * 2 * TS);
+        pv.store(tiles + cur * 2 * TS + TS);
+      }
+      x = nx;
+    }
+    const uint32_t bad = rows > 0 ? nan_rows(acc) & (rows < 32 ? (1u << rows) - 1 : ~0u) : 0;
+    store_own<T, NS>(dq + (int64_t)(q0 + c) * ldq, c < rows && !((bad >> c) & 1), acc, a.scale, a.dim);
+    for (uint32_t left = bad; left; left &= left - 1) {
+      const int n = __builtin_ctz(left), i = q0 + n;
+      float r[2];
+      row_dq<T>(a, q + (int64_t)i * ldq, d_o + (int64_t)i * ldq, k, v, ldk, i + shift, lk, lane_value(sub, n),
+                lane_value(dl, n), r);
+      row_store<T>(dq + (int64_t)i * ldq, r, a.dim);
+    }
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
-  typedef typename Elem<T>::type E;
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads, 1) void k_attn_dkv(AttnArgs a) {
+  typedef Geo<T, NS> G;
+  typedef typename G::E E;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  __shared__ __attribute__((aligned(16))) float stats[2][2][kTile];
+  E* const tiles = reinterpret_cast<E*>(lds_raw);
+  constexpr int TS = kTile * G::LD;
   const Place w = place_of(a, a.kv_heads);
   const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
-  const int group = a.heads / a.kv_heads;
-  for (int64_t t = w.tile; t * kRows < sk.len; t += a.tiles) {
-    const int j = (int)t * kRows + threadIdx.x / 64;
-    if (j >= sk.len) continue;
-    const int64_t at = (sk.start + j) * ldk + (int64_t)w.head * a.dim;
-    float dk[2] = {0.f, 0.f}, dv[2] = {0.f, 0.f};
-    for (int g = 0; g < group; ++g) {
-      const int64_t h = (int64_t)w.head * group + g, row = sq.start * ldq + h * a.dim, st = sq.start * a.heads + h;
-      row_dkv<T>(a, static_cast<const E*>(a.q) + row, static_cast<const E*>(a.d_o) + row, a.lse + st, a.delta + st, ldq,
-                 static_cast<const E*>(a.k) + at, static_cast<const E*>(a.v) + at, j, sq.len, sk.len, dk, dv);
+  const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
+  const int group = a.heads / a.kv_heads, lq = sq.len, lk = sk.len, shift = sk.len - sq.len;
+  const int64_t head = sk.start * ldk + (int64_t)w.head * a.dim;
+  const E *k = static_cast<const E*>(a.k) + head, *v = static_cast<const E*>(a.v) + head;
+  E *dk = static_cast<E*>(a.dk) + head, *dv = static_cast<E*>(a.dv) + head;
+  const int64_t qhead = sq.start * ldq + (int64_t)w.head * group * a.dim;
+  const E *q = static_cast<const E*>(a.q) + qhead, *d_o = static_cast<const E*>(a.d_o) + qhead;
+  const float* lse = a.lse + (int64_t)w.head * group * a.tq + sq.start;
+  const float* delta = a.delta + (int64_t)w.head * group * a.tq + sq.start;
+  const int c = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float scale2 = fabsf(a.scale2);
+  for (int64_t t = w.tile; t * kBlock < lk; t += a.tiles) {
+    const int b0 = (int)t * kBlock, k0 = b0 + kOwn * wave, rows = min(lk - k0, kOwn), j = k0 + c;
+    // tiles of queries that see one of the keys b0 .. b1
+    const int b1 = min(b0 + kBlock, lk) - 1;
+    const int i0 = max(0, b0 - a.right - shift), i1 = b0 < a.sinks ? lq : min(lq, b1 + a.left - shift + 1);
+    const int x0 = i0 / kTile, x1 = i1 > i0 ? (i1 + kTile - 1) / kTile : x0, n = (x1 - x0) * group;
+    Own<T, NS> kf, vf;
+    kf.load(k + (int64_t)k0 * ldk, rows, lbk, a.dim);
+    vf.load(v + (int64_t)k0 * ldk, rows, lbk, a.dim);
+    if (a.scale2 < 0.f) kf.negate();
+    f32x16 ak[NS], av[NS];
+#pragma unroll
+    for (int dt = 0; dt < NS; ++dt) ak[dt] = av[dt] = zero16();
+    Pieces<T, NS> pq, pd;
+    float stat = 0.f;
+    // tile `x` of query head `h` of the group
+    const auto bring = [&](int h, int x) {
+      const int64_t at = (int64_t)x * kTile * ldq + (int64_t)h * a.dim;
+      pq.load(q + at, lq - x * kTile, lbq, a.dim);
+      pd.load(d_o + at, lq - x * kTile, lbq, a.dim);
+      if (threadIdx.x < 2 * kTile) {
+        const int i = x * kTile + (threadIdx.x & (kTile - 1));
+        const float* from = threadIdx.x < kTile ? lse : delta;
+        stat = i < lq ? from[(int64_t)h * a.tq + i] : threadIdx.x < kTile ? INFINITY : 0.f;
+      }
+    };
+    const auto put = [&](int b) {
+      pq.store(tiles + b * 2 * TS);
+      pd.store(tiles + b * 2 * TS + TS);
+      if (threadIdx.x < 2 * kTile) (&stats[b][0][0])[threadIdx.x] = stat;
+    };
+    int h = 0, x = x0, cur = 0;
+    __syncthreads();  // the last tile's readers are done
+    if (n > 0) {
+      bring(0, x0);
+      put(0);
     }
-    row_store<T>(static_cast<E*>(a.dk) + at, dk, a.dim);
-    row_store<T>(static_cast<E*>(a.dv) + at, dv, a.dim);
+    for (int it = 0; it < n; ++it) {
+      int nx = x + 1, nh = h;
+      if (nx == x1) {
+        nx = x0;
+        ++nh;
+      }
+      lds_barrier();
+      if (it + 1 < n) bring(nh, nx);
+      const E *tq = tiles + cur * 2 * TS, *td = tq + TS;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int i = x * kTile + 32 * hf, p0 = i + shift, p1 = min(i + 31, lq - 1) + shift;
+        if (rows <= 0 || i >= lq || none_seen(a, k0, rows, p0, p1, lk)) continue;
+        f32x16 s = rows_times_own<T, NS>(tq, hf, kf);
+        f32x16 dp = rows_times_own<T, NS>(td, hf, vf);
+        const float *ls = &stats[cur][0][32 * hf + 4 * g], *ds = &stats[cur][1][32 * hf + 4 * g];
+        const bool whole = i + 32 <= lq && all_seen(a, k0, kOwn, p0, p1, lk);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + 8 * y), d4 = *reinterpret_cast<const f32x4*>(ds + 8 * y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int z = 4 * y + e;
+            s[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], scale2, -l4[e]));
+            dp[z] = s[z] * (dp[z] - d4[e]);
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int z = 0; z < 16; ++z) {
+            const int r = i + 8 * (z / 4) + 4 * g + z % 4;
+            const bool on = r < lq && seen(a, j, r + shift, lk);
+            s[z] = on ? s[z] : 0.f;
+            dp[z] = on ? dp[z] : 0.f;
+          }
+        }
+        cols_times_result<T, NS>(td, hf, s, av);
+        cols_times_result<T, NS>(tq, hf, dp, ak);
+      }
+      if (it + 1 < n) {
+        cur ^= 1;
+        put(cur);
+      }
+      x = nx;
+      h = nh;
+    }
+    const uint32_t bad = rows > 0 ? (nan_rows(ak) | nan_rows(av)) & (rows < 32 ? (1u << rows) - 1 : ~0u) : 0;
+    const bool on = c < rows && !((bad >> c) & 1);
+    store_own<T, NS>(dk + (int64_t)j * ldk, on, ak, a.scale, a.dim);
+    store_own<T, NS>(dv + (int64_t)j * ldk, on, av, 1.f, a.dim);
+    for (uint32_t left = bad; left; left &= left - 1) {
+      const int y = k0 + __builtin_ctz(left);
+      float rk[2] = {0.f, 0.f}, rv[2] = {0.f, 0.f};
+      for (int hh = 0; hh < group; ++hh)
+        row_dkv<T>(a, q + hh * a.dim, d_o + hh * a.dim, lse + (int64_t)hh * a.tq, delta + (int64_t)hh * a.tq, ldq,
+                   k + (int64_t)y * ldk, v + (int64_t)y * ldk, y, lq, lk, rk, rv);
+      row_store<T>(dk + (int64_t)y * ldk, rk, a.dim);
+      row_store<T>(dv + (int64_t)y * ldk, rv, a.dim);
+    }
   }
+}
+
+// f(T{}, integral constant NS) for the descriptor's type and head size
+template <typename F>
+void with_geo(const ttc_attn_desc* d, F f) {
+  using std::integral_constant;
+  const int ns = (d->dim + 31) / 32;
+  const auto by_size = [&](auto t) {
+    if (ns == 1) f(t, integral_constant<int, 1>{});
+    else if (ns == 2) f(t, integral_constant<int, 2>{});
+    else if (ns == 3) f(t, integral_constant<int, 3>{});
+    else f(t, integral_constant<int, 4>{});
+  };
+  if (d->dtype == TTC_F32) by_size(float{});
+  else by_size(bf16_t{});
+}
+
+// two buffers of two tiles
+template <typename T, int NS>
+constexpr size_t tile_lds() {
+  return 4 * kTile * Geo<T, NS>::LD * sizeof(typename Elem<T>::type);
+}
+
+template <typename K>
+void launch(K kern, unsigned grid, size_t lds, hipStream_t s, const AttnArgs& a) {
+  if (lds > 65536)
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  TTC_LAUNCH(kern, dim3(grid), dim3(kThreads), lds, s, a);
 }
 
 struct DecodeArgs {
@@ -389,10 +927,13 @@ extern "C" ttc_status ttc_attn_fwd(const ttc_attn_desc* desc, const ttc_attn_seq
   a.lse = static_cast<float*>(saved);
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
-  const unsigned grid = grid_of(a, seqs->max_q, a.tq, kRows, a.heads);
+  const unsigned grid = grid_of(a, seqs->max_q, a.tq, kBlock, a.heads);
   TraceScope ts("attn_fwd", s);
-  auto kern = desc->dtype == TTC_F32 ? k_attn_fwd<float> : k_attn_fwd<bf16_t>;
-  TTC_LAUNCH(kern, dim3(grid), dim3(kThreads), 0, s, a);
+  with_geo(desc, [&](auto ty, auto ns) {
+    typedef decltype(ty) T;
+    constexpr int NS = decltype(ns)::value;
+    launch(k_attn_fwd<T, NS>, grid, tile_lds<T, NS>(), s, a);
+  });
   return launched();
 }
 
@@ -426,16 +967,22 @@ extern "C" ttc_status ttc_attn_bwd(const ttc_attn_desc* desc, const ttc_attn_seq
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
   if (a.tq > 0) {
-    const unsigned grid = grid_of(a, seqs->max_q, a.tq, kRows, a.heads);
+    const unsigned grid = grid_of(a, seqs->max_q, a.tq, kBlock, a.heads);
     TraceScope ts("attn_dq", s);
-    auto kern = desc->dtype == TTC_F32 ? k_attn_dq<float> : k_attn_dq<bf16_t>;
-    TTC_LAUNCH(kern, dim3(grid), dim3(kThreads), 0, s, a);
+    with_geo(desc, [&](auto ty, auto ns) {
+      typedef decltype(ty) T;
+      constexpr int NS = decltype(ns)::value;
+      launch(k_attn_dq<T, NS>, grid, tile_lds<T, NS>(), s, a);
+    });
   }
   if (a.tk > 0) {
-    const unsigned grid = grid_of(a, seqs->max_k, a.tk, kRows, a.kv_heads);
+    const unsigned grid = grid_of(a, seqs->max_k, a.tk, kBlock, a.kv_heads);
     TraceScope ts("attn_dkv", s);
-    auto kern = desc->dtype == TTC_F32 ? k_attn_dkv<float> : k_attn_dkv<bf16_t>;
-    TTC_LAUNCH(kern, dim3(grid), dim3(kThreads), 0, s, a);
+    with_geo(desc, [&](auto ty, auto ns) {
+      typedef decltype(ty) T;
+      constexpr int NS = decltype(ns)::value;
+      launch(k_attn_dkv<T, NS>, grid, tile_lds<T, NS>(), s, a);
+    });
   }
   return launched();
 }
