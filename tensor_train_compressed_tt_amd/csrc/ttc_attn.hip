@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "../../include/ttc_block.h"
@@ -810,25 +811,197 @@ void launch(K kern, unsigned grid, size_t lds, hipStream_t s, const AttnArgs& a)
   TTC_LAUNCH(kern, dim3(grid), dim3(kThreads), lds, s, a);
 }
 
+// ---- one new token a sequence ----------------------------------------------------
+//
+// Bound by the cache's bytes.  A row of K or V is spread over LPR lanes, 16
+// bytes each, so a load of a wave brings 64 / LPR rows; each of these row
+// groups keeps a softmax of its own (maximum, sum, products) in registers, and
+// the groups, the waves and the splits of a long cache are joined at the end,
+// always in the same order.  A key head's rows are read once for up to HG of
+// the query heads that share it.
+
 struct DecodeArgs {
   AttnArgs a;
   const int32_t* lens;
   int64_t capacity;
+  float* part;  // splits > 1: sum, maximum and products of each (row, head, split)
+  int splits, chunks;
 };
 
-template <typename T>
-__global__ __launch_bounds__(64) void k_attn_decode(DecodeArgs d) {
+constexpr int kAhead = 4;  // row loads of K and of V that a lane has in flight
+constexpr int kPartHead = 4;  // floats before a partial's products: maximum, sum
+
+// sum over the LPR lanes of a row
+template <int LPR>
+__device__ __forceinline__ float row_lanes_sum(float v) {
+  const auto add = [](float x, auto ctrl) {
+    return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  using std::integral_constant;
+  if constexpr (LPR > 1) v = add(v, integral_constant<int, 0xb1>{});    // lanes 1 apart
+  if constexpr (LPR > 2) v = add(v, integral_constant<int, 0x4e>{});    // 2 apart
+  if constexpr (LPR > 4) v = add(v, integral_constant<int, 0x141>{});   // the mirrored lane of 8
+  if constexpr (LPR > 8) v = add(v, integral_constant<int, 0x140>{});   // and of 16
+  if constexpr (LPR > 16) v += __shfl_xor(v, 16);
+  return v;
+}
+
+// joins (m2, l2, acc2) into (m, l, acc)
+template <int N>
+__device__ __forceinline__ void join(float& m, float& l, float (&acc)[N], float m2, float l2, const float (&acc2)[N]) {
+  const float mn = fmaxf(m, m2);
+  const float f = m == -INFINITY ? 0.f : exp2f(m - mn), f2 = m2 == -INFINITY ? 0.f : exp2f(m2 - mn);
+  m = mn;
+  // a factor of zero is a side that has seen nothing: its sums are zero, or a NaN that stays
+  l = l * f + l2 * f2;
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = acc[e] * f + acc2[e] * f2;
+}
+
+template <typename T, int LPR, int HG>
+__global__ __launch_bounds__(1024) void k_attn_decode(DecodeArgs d) {
   typedef typename Elem<T>::type E;
+  typedef typename Mma<T>::frag frag;
+  constexpr int V = Mma<T>::EPV, RPW = 64 / LPR;
+  extern __shared__ __attribute__((aligned(16))) float dec_lds[];  // [wave][HG][kPartHead + LPR * V]
   const AttnArgs& a = d.a;
-  const int b = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
+  const int lane = threadIdx.x & 63, r = lane / LPR, x = lane % LPR;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int split = blockIdx.x % d.splits, rest = blockIdx.x / d.splits;
+  const int chunk = rest % d.chunks, hk = rest / d.chunks % a.kv_heads, b = rest / d.chunks / a.kv_heads;
+  const int group = a.heads / a.kv_heads, h0 = hk * group + chunk * HG, hn = min(HG, group - chunk * HG);
   const int n = (int)min(max((int64_t)d.lens[b], (int64_t)0), d.capacity);
+  // the keys that are seen, counted from 0: `first` sinks, then those from `lo` on
+  const int lo = max(0, n - 1 - a.left), first = min(min(a.sinks, lo), n), count = first + n - lo;
+  const int per = (count + d.splits - 1) / d.splits;
+  const int c0 = min(count, split * per), c1 = min(count, c0 + per);
   const int64_t ldk = (int64_t)a.kv_heads * a.dim;
-  const int64_t at = ((int64_t)b * a.heads + h) * a.dim;
-  const int64_t kv = b * d.capacity * ldk + (int64_t)(h / (a.heads / a.kv_heads)) * a.dim;
-  float acc[2], lse;
-  row_fwd<T>(a, static_cast<const E*>(a.q) + at, static_cast<const E*>(a.k) + kv, static_cast<const E*>(a.v) + kv, ldk,
-             n - 1, n, acc, lse);
-  row_store<T>(static_cast<E*>(a.o) + at, acc, a.dim);
+  const bool on = x * V < a.dim;
+  const int64_t at = b * d.capacity * ldk + (int64_t)hk * a.dim + (on ? x * V : 0);
+  const E *k = static_cast<const E*>(a.k) + at, *v = static_cast<const E*>(a.v) + at;
+  float q[HG][V], acc[HG][V], m[HG], l[HG];
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    const bool have = on && h < hn;
+    const frag f = *reinterpret_cast<const frag*>(static_cast<const E*>(a.q) +
+                                                  ((int64_t)b * a.heads + h0 + (have ? h : 0)) * a.dim + (on ? x * V : 0));
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      q[h][e] = have ? elem_to_f32<T>(f[e]) * a.scale2 : 0.f;
+      acc[h][e] = 0.f;
+    }
+    m[h] = -INFINITY;
+    l[h] = 0.f;
+  }
+  const int turn = waves * RPW * kAhead;
+  for (int c = c0 + wave * RPW * kAhead; c < c1; c += turn) {
+    frag fk[kAhead], fv[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = min(c + u * RPW + r, c1 - 1);  // past the end: a row that is seen, at no weight
+      const int64_t row = (int64_t)(i < first ? i : i - first + lo) * ldk;
+      fk[u] = *reinterpret_cast<const frag*>(k + row);
+      fv[u] = *reinterpret_cast<const frag*>(v + row);
+      if (!on) fk[u] = Mma<T>::zero();
+      if (c + u * RPW + r >= c1) fv[u] = Mma<T>::zero();
+    }
+    float s[HG][kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float kx[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) kx[e] = elem_to_f32<T>(fk[u][e]);
+      const bool have = c + u * RPW + r < c1;
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        float y = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) y += q[h][e] * kx[e];
+        s[h][u] = have ? row_lanes_sum<LPR>(y) : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      float mn = m[h];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) mn = fmaxf(mn, s[h][u]);
+      const float sub = mn == -INFINITY ? 0.f : mn;
+      const float keep = __builtin_amdgcn_exp2f(m[h] - sub);
+      m[h] = mn;
+      l[h] *= keep;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[h][e] *= keep;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        s[h][u] = __builtin_amdgcn_exp2f(s[h][u] - sub);
+        l[h] += s[h][u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float y = elem_to_f32<T>(fv[u][e]);
+#pragma unroll
+        for (int h = 0; h < HG; ++h) acc[h][e] += s[h][u] * y;
+      }
+  }
+  // the wave's row groups, then the waves in order
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+#pragma unroll
+    for (int step = LPR; step < 64; step <<= 1) {
+      float other[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) other[e] = __shfl_xor(acc[h][e], step);
+      join(m[h], l[h], acc[h], __shfl_xor(m[h], step), __shfl_xor(l[h], step), other);
+    }
+    float* to = dec_lds + (wave * HG + h) * (kPartHead + LPR * V);
+    if (r == 0) {
+      if (x == 0) {
+        to[0] = m[h];
+        to[1] = l[h];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) to[kPartHead + x * V + e] = acc[h][e];
+    }
+  }
+  __syncthreads();
+  for (int y = threadIdx.x; y < hn * a.dim; y += blockDim.x) {
+    const int h = y / a.dim, c = y - h * a.dim;
+    float mm = -INFINITY, ll = 0.f, o[1] = {0.f};
+    for (int w = 0; w < waves; ++w) {
+      const float* from = dec_lds + (w * HG + h) * (kPartHead + LPR * V);
+      const float o2[1] = {from[kPartHead + c]};
+      join(mm, ll, o, from[0], from[1], o2);
+    }
+    const int64_t head = (int64_t)b * a.heads + h0 + h;
+    if (d.splits == 1) {
+      static_cast<E*>(a.o)[head * a.dim + c] = Mma<T>::from_f32(ll == 0.f ? 0.f : o[0] / ll);
+    } else {
+      float* to = d.part + (head * d.splits + split) * (kPartHead + a.dim);
+      if (c == 0) {
+        to[0] = mm;
+        to[1] = ll;
+      }
+      to[kPartHead + c] = o[0];
+    }
+  }
+}
+
+// joins the splits of one (row, head), a thread an element
+template <typename T>
+__global__ __launch_bounds__(kMaxDim) void k_attn_join(DecodeArgs d) {
+  const int c = threadIdx.x;
+  if (c >= d.a.dim) return;
+  const int64_t head = blockIdx.x;
+  float m = -INFINITY, l = 0.f, o[1] = {0.f};
+  for (int s = 0; s < d.splits; ++s) {
+    const float* from = d.part + (head * d.splits + s) * (kPartHead + d.a.dim);
+    const float o2[1] = {from[kPartHead + c]};
+    join(m, l, o, from[0], from[1], o2);
+  }
+  static_cast<typename Elem<T>::type*>(d.a.o)[head * d.a.dim + c] = Mma<T>::from_f32(l == 0.f ? 0.f : o[0] / l);
 }
 
 // ---- host --------------------------------------------------------------------
@@ -997,12 +1170,50 @@ ttc_status check_decode(const ttc_attn_desc* d, int64_t batch, int64_t capacity)
 }
 }  // namespace
 
+namespace {
+// How a decode is cut: heads a wave takes together, work-groups of a key head,
+// waves of a work-group, splits of a sequence's keys.
+struct DecodeCut {
+  int heads, chunks, threads, splits;
+};
+DecodeCut decode_cut(const ttc_attn_desc* d, int64_t batch, int64_t capacity) {
+  const int group = d->heads / d->kv_heads;
+  DecodeCut c;
+  c.heads = group >= 3 ? 4 : group;
+  c.chunks = (group + c.heads - 1) / c.heads;
+  const int64_t base = batch * d->kv_heads * c.chunks;
+  int64_t most = capacity;  // keys that a query can see
+  if (d->left >= 0) most = std::min<int64_t>(most, (int64_t)d->left + 1 + d->sinks);
+  // two work-groups of four waves to each of 256 CUs, else 16 waves and splits of 1024 keys or more
+  c.threads = base >= 512 ? 256 : 1024;
+  c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most / 1024, base >= 512 ? 1 : 512 / base));
+  return c;
+}
+size_t decode_need(const ttc_attn_desc* d, int64_t batch, const DecodeCut& c) {
+  return c.splits == 1 ? 0 : (size_t)batch * d->heads * c.splits * (kPartHead + d->dim) * sizeof(float);
+}
+// f(integral constants lanes of a row, heads of a wave)
+template <typename T, typename F>
+void with_decode(int lanes, int heads, F f) {
+  using std::integral_constant;
+  const auto by_heads = [&](auto l) {
+    if (heads == 1) f(l, integral_constant<int, 1>{});
+    else if (heads == 2) f(l, integral_constant<int, 2>{});
+    else f(l, integral_constant<int, 4>{});
+  };
+  if (lanes <= 4) by_heads(integral_constant<int, 4>{});
+  else if (lanes <= 8) by_heads(integral_constant<int, 8>{});
+  else if (lanes <= 16 || kMaxDim / Mma<T>::EPV <= 16) by_heads(integral_constant<int, 16>{});
+  else by_heads(integral_constant<int, kMaxDim / Mma<T>::EPV>{});
+}
+}  // namespace
+
 extern "C" ttc_status ttc_attn_decode_workspace(const ttc_attn_desc* desc, int64_t batch, int64_t capacity,
                                                 size_t* scratch_bytes) {
   if (!scratch_bytes) return TTC_ERR_NULL;
   const ttc_status st = check_decode(desc, batch, capacity);
   if (st != TTC_OK) return st;
-  *scratch_bytes = 0;
+  *scratch_bytes = batch == 0 ? 0 : decode_need(desc, batch, decode_cut(desc, batch, capacity));
   return TTC_OK;
 }
 
@@ -1012,18 +1223,33 @@ extern "C" ttc_status ttc_attn_decode(const ttc_attn_desc* desc, int64_t batch, 
   const ttc_status st = check_decode(desc, batch, capacity);
   if (st != TTC_OK) return st;
   if (batch == 0) return TTC_OK;
-  if (!q || !lens || !o || (capacity > 0 && (!k || !v))) return TTC_ERR_NULL;
+  const DecodeCut cut = decode_cut(desc, batch, capacity);
+  const size_t need = decode_need(desc, batch, cut);
+  if (!q || !lens || !o || (capacity > 0 && (!k || !v)) || (need && !scratch)) return TTC_ERR_NULL;
   if (!al16(q) || !al16(k) || !al16(v) || !al16(lens) || !al16(o) || !al16(scratch)) return TTC_ERR_ALIGN;
-  (void)scratch_bytes;
-  DecodeArgs d = {make_args(desc), lens, capacity};
+  if (scratch_bytes < need) return TTC_ERR_WORKSPACE;
+  DecodeArgs d = {make_args(desc), lens, capacity, static_cast<float*>(scratch), cut.splits, cut.chunks};
   d.a.q = q;
   d.a.k = k;
   d.a.v = v;
   d.a.o = o;
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
-  TraceScope ts("attn_decode", s);
-  auto kern = desc->dtype == TTC_F32 ? k_attn_decode<float> : k_attn_decode<bf16_t>;
-  TTC_LAUNCH(kern, dim3((unsigned)(batch * desc->heads)), dim3(64), 0, s, d);
+  const unsigned grid = (unsigned)(batch * desc->kv_heads * cut.chunks * cut.splits);
+  const auto run = [&](auto t) {
+    typedef decltype(t) T;
+    with_decode<T>(desc->dim / Mma<T>::EPV, cut.heads, [&](auto lpr, auto hg) {
+      constexpr int L = decltype(lpr)::value, H = decltype(hg)::value;
+      const size_t lds = (size_t)(cut.threads / 64) * H * (kPartHead + L * Mma<T>::EPV) * sizeof(float);  // at most 34 KB
+      TraceScope ts("attn_decode", s);
+      TTC_LAUNCH((k_attn_decode<T, L, H>), dim3(grid), dim3(cut.threads), lds, s, d);
+    });
+    if (cut.splits > 1) {
+      TraceScope ts("attn_join", s);
+      TTC_LAUNCH(k_attn_join<T>, dim3((unsigned)(batch * desc->heads)), dim3(kMaxDim), 0, s, d);
+    }
+  };
+  if (desc->dtype == TTC_F32) run(float{});
+  else run(bf16_t{});
   return launched();
 }
