@@ -145,9 +145,9 @@ class WindowAttention:
         _need(k, "k", self.dtype, (k.shape[0], self.kv_heads * self.dim))
         _need(v, "v", self.dtype, tuple(k.shape))
 
-    def workspace(self, q, k, batch=1):
-        """Bytes of (saved, scratch) for these queries and keys."""
-        return ttc_attn_workspace(self.desc, make_attn_seqs(batch, int(q.shape[0]), int(k.shape[0])))
+    def workspace(self, q, k, batch=1, q_offsets=None, k_offsets=None, max_q=None, max_k=None):
+        """Bytes of (saved, scratch) of a call with these arguments."""
+        return ttc_attn_workspace(self.desc, self._seqs(q, k, batch, q_offsets, k_offsets, max_q, max_k))
 
     def forward(self, q, k, v, batch=1, q_offsets=None, k_offsets=None, max_q=None, out=None, saved=None):
         """(o, saved).  ``max_q``, the longest sequence's queries, sizes the launch

@@ -48,6 +48,8 @@ struct AttnArgs {
   int left, right, sinks;
   float scale, scale2;  // scale2 = scale log2 e
   int tiles;            // tiles of a sequence's rows that the grid has
+  int far;              // k_attn_dkv: work-groups of a head for the sinks' far queries
+  float* part;          // their sums, [sequence][key head][1 + far][2][sinks][dim]
 };
 
 // rows [start, start + len) of sequence b; offsets that do not ascend or pass
@@ -165,16 +167,14 @@ __device__ void row_dq(const AttnArgs& a, const typename Elem<T>::type* q, const
   }
 }
 
-// what one query head adds to dk and dv of key j; q, d_o, lse, delta from the
-// sequence's first row on
+// what queries [i0, i_end) of one query head add to dk and dv of key j, which
+// all of them see; q, d_o, lse, delta from the sequence's first row on
 template <typename T>
 __device__ void row_dkv(const AttnArgs& a, const typename Elem<T>::type* q, const typename Elem<T>::type* d_o,
                         const float* lse, const float* delta, int64_t ldq, const typename Elem<T>::type* k,
-                        const typename Elem<T>::type* v, int j, int lq, int lk, float (&dk)[2], float (&dv)[2]) {
+                        const typename Elem<T>::type* v, int i0, int i_end, float (&dk)[2], float (&dv)[2]) {
   const int lane = threadIdx.x & 63;
-  const int shift = lk - lq;
-  const int i_end = j < a.sinks ? lq : min(lq, j + a.left - shift + 1);
-  for (int i0 = max(0, j - a.right - shift); i0 < i_end; i0 += 64) {
+  for (; i0 < i_end; i0 += 64) {
     const int n = min(64, i_end - i0);
     float ds = 0.f, e = 0.f;
     if (lane < n) {
@@ -420,8 +420,8 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const AttnArgs& a, int heads) {
   const int n = gridDim.x, x = blockIdx.x & 7, y = blockIdx.x >> 3, per = n >> 3, more = n & 7;
-  const int g = x * per + min(x, more) + y, r = g / a.tiles;
-  return {g - r * a.tiles, r % heads, r / heads};
+  const int units = a.tiles + a.far, g = x * per + min(x, more) + y, r = g / units;
+  return {g - r * units, r % heads, r / heads};
 }
 
 // The tiles that queries at places p0 .. p1 see: [0, s) and [lo, hi).
@@ -661,14 +661,27 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(AttnArgs a) {
   }
 }
 
+// Queries of a far piece.  The first keys of a long sequence are seen by all of
+// its later queries, so the work-group of these keys would run long after all
+// others; queries past the window of its keys, which see the sinks alone, are
+// left to a.far further work-groups, and k_attn_sinks adds up their sums.
+constexpr int kFar = 512;
+constexpr int kMaxFarSinks = kBlock;  // all sinks in the first block of keys
+
+// work-groups that a CU holds: two where a wave's registers allow it
 template <typename T, int NS>
-__global__ __launch_bounds__(kThreads, 1) void k_attn_dkv(AttnArgs a) {
+constexpr int dkv_groups() {
+  return (sizeof(typename Elem<T>::type) == 2 ? NS <= 2 : NS <= 1) ? 2 : 1;
+}
+
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads, (dkv_groups<T, NS>())) void k_attn_dkv(AttnArgs a) {
   typedef Geo<T, NS> G;
   typedef typename G::E E;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   __shared__ __attribute__((aligned(16))) float stats[2][2][kTile];
   E* const tiles = reinterpret_cast<E*>(lds_raw);
-  constexpr int TS = kTile * G::LD;
+  constexpr int TS = kTile * G::LD, kPiece = kFar / kTile;
   const Place w = place_of(a, a.kv_heads);
   const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
@@ -684,12 +697,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_dkv(AttnArgs a) {
   const int c = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float scale2 = fabsf(a.scale2);
-  for (int64_t t = w.tile; t * kBlock < lk; t += a.tiles) {
+  // the far work-groups' queries begin at tile xf: past the window of the first block's keys
+  const bool far = w.tile >= a.tiles;
+  const int xf = (max(0, min(lq, min(kBlock, lk) + a.left - shift)) + kTile - 1) / kTile;
+  const int unit = far ? 1 + w.tile - a.tiles : 0;
+  for (int64_t t = far ? 0 : w.tile; t * kBlock < lk; t += a.tiles) {
     const int b0 = (int)t * kBlock, k0 = b0 + kOwn * wave, rows = min(lk - k0, kOwn), j = k0 + c;
-    // tiles of queries that see one of the keys b0 .. b1
+    const bool split = a.far > 0 && t == 0;  // the block's sinks go to a.part
+    const int sinks = split ? min(a.sinks, lk) : 0;
+    // tiles of queries that see one of the keys b0 .. b1; a far work-group takes kPiece of each a.far kPiece
     const int b1 = min(b0 + kBlock, lk) - 1;
     const int i0 = max(0, b0 - a.right - shift), i1 = b0 < a.sinks ? lq : min(lq, b1 + a.left - shift + 1);
-    const int x0 = i0 / kTile, x1 = i1 > i0 ? (i1 + kTile - 1) / kTile : x0, n = (x1 - x0) * group;
+    const int x0 = far ? xf + (unit - 1) * kPiece : i0 / kTile;
+    const int xe = i1 > i0 ? (i1 + kTile - 1) / kTile : 0, x1 = split && !far ? min(xe, xf) : xe;
     Own<T, NS> kf, vf;
     kf.load(k + (int64_t)k0 * ldk, rows, lbk, a.dim);
     vf.load(v + (int64_t)k0 * ldk, rows, lbk, a.dim);
@@ -715,20 +735,21 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_dkv(AttnArgs a) {
       pd.store(tiles + b * 2 * TS + TS);
       if (threadIdx.x < 2 * kTile) (&stats[b][0][0])[threadIdx.x] = stat;
     };
-    int h = 0, x = x0, cur = 0;
+    int h = x0 < x1 ? 0 : group, x = x0, cur = 0;
     __syncthreads();  // the last tile's readers are done
-    if (n > 0) {
+    if (h < group) {
       bring(0, x0);
       put(0);
     }
-    for (int it = 0; it < n; ++it) {
+    while (h < group) {
       int nx = x + 1, nh = h;
-      if (nx == x1) {
+      if (far && (nx - xf) % kPiece == 0) nx += kPiece * (a.far - 1);
+      if (nx >= x1) {
         nx = x0;
         ++nh;
       }
       lds_barrier();
-      if (it + 1 < n) bring(nh, nx);
+      if (nh < group) bring(nh, nx);
       const E *tq = tiles + cur * 2 * TS, *td = tq + TS;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -760,7 +781,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_dkv(AttnArgs a) {
         cols_times_result<T, NS>(td, hf, s, av);
         cols_times_result<T, NS>(tq, hf, dp, ak);
       }
-      if (it + 1 < n) {
+      if (nh < group) {
         cur ^= 1;
         put(cur);
       }
@@ -769,17 +790,59 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_dkv(AttnArgs a) {
     }
     const uint32_t bad = rows > 0 ? (nan_rows(ak) | nan_rows(av)) & (rows < 32 ? (1u << rows) - 1 : ~0u) : 0;
     const bool on = c < rows && !((bad >> c) & 1);
-    store_own<T, NS>(dk + (int64_t)j * ldk, on, ak, a.scale, a.dim);
-    store_own<T, NS>(dv + (int64_t)j * ldk, on, av, 1.f, a.dim);
+    float* const part = a.part + (((int64_t)w.b * a.kv_heads + w.head) * (1 + a.far) + unit) * 2 * a.sinks * a.dim;
+    float* const part_v = part + (int64_t)a.sinks * a.dim;
+    if (!far) {
+      store_own<T, NS>(dk + (int64_t)j * ldk, on && j >= sinks, ak, a.scale, a.dim);
+      store_own<T, NS>(dv + (int64_t)j * ldk, on && j >= sinks, av, 1.f, a.dim);
+    }
+    if (split) {
+      store_own<float, NS>(part + (int64_t)j * a.dim, on && j < sinks, ak, a.scale, a.dim);
+      store_own<float, NS>(part_v + (int64_t)j * a.dim, on && j < sinks, av, 1.f, a.dim);
+    }
     for (uint32_t left = bad; left; left &= left - 1) {
       const int y = k0 + __builtin_ctz(left);
+      if (far && y >= sinks) continue;
       float rk[2] = {0.f, 0.f}, rv[2] = {0.f, 0.f};
-      for (int hh = 0; hh < group; ++hh)
-        row_dkv<T>(a, q + hh * a.dim, d_o + hh * a.dim, lse + (int64_t)hh * a.tq, delta + (int64_t)hh * a.tq, ldq,
-                   k + (int64_t)y * ldk, v + (int64_t)y * ldk, y, lq, lk, rk, rv);
-      row_store<T>(dk + (int64_t)y * ldk, rk, a.dim);
-      row_store<T>(dv + (int64_t)y * ldk, rv, a.dim);
+      const int y0 = max(0, y - a.right - shift), y1 = y < a.sinks ? lq : min(lq, y + a.left - shift + 1);
+      for (int hh = 0; hh < group; ++hh) {
+        const auto add = [&](int from, int to) {
+          row_dkv<T>(a, q + hh * a.dim, d_o + hh * a.dim, lse + (int64_t)hh * a.tq, delta + (int64_t)hh * a.tq, ldq,
+                     k + (int64_t)y * ldk, v + (int64_t)y * ldk, from, to, rk, rv);
+        };
+        if (!far)
+          add(y0, y < sinks ? min(y1, xf * kTile) : y1);
+        else
+          for (int64_t i = (int64_t)x0 * kTile; i < y1; i += (int64_t)a.far * kFar) add((int)i, min(y1, (int)i + kFar));
+      }
+      if (y < sinks) {
+        row_store<float>(part + (int64_t)y * a.dim, rk, a.dim);
+        row_store<float>(part_v + (int64_t)y * a.dim, rv, a.dim);
+      } else {
+        row_store<T>(dk + (int64_t)y * ldk, rk, a.dim);
+        row_store<T>(dv + (int64_t)y * ldk, rv, a.dim);
+      }
     }
+    if (far) break;
+  }
+}
+
+// The sinks' dk and dv: the sums of the first block's work-group and of the far
+// ones, in order; a work-group a (sequence, key head).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_attn_sinks(AttnArgs a) {
+  typedef typename Elem<T>::type E;
+  const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
+  const Span sk = span_of(a.k_off, b, a.batch, a.tk);
+  const int64_t ldk = (int64_t)a.kv_heads * a.dim, unit = (int64_t)2 * a.sinks * a.dim;
+  const float* part = a.part + (int64_t)blockIdx.x * (1 + a.far) * unit;
+  const int n = min(a.sinks, sk.len) * a.dim;
+  for (int x = threadIdx.x; x < 2 * n; x += kThreads) {
+    const int which = x >= n, y = x - which * n, j = y / a.dim, c = y - j * a.dim;
+    const float* from = part + which * (int64_t)a.sinks * a.dim + y;
+    float s = 0.f;
+    for (int u = 0; u <= a.far; ++u) s += from[u * unit];
+    static_cast<E*>(which ? a.dv : a.dk)[(sk.start + j) * ldk + (int64_t)head * a.dim + c] = Mma<T>::from_f32(s);
   }
 }
 
@@ -796,6 +859,20 @@ void with_geo(const ttc_attn_desc* d, F f) {
   };
   if (d->dtype == TTC_F32) by_size(float{});
   else by_size(bf16_t{});
+}
+
+// far work-groups of a key head (see k_attn_dkv), none where the later queries are few
+int far_of(const ttc_attn_desc* d, const ttc_attn_seqs* s) {
+  if (d->sinks < 1 || d->sinks > kMaxFarSinks || d->left < 0 || s->tk == 0) return 0;
+  const int64_t most = s->q_offsets ? (s->max_q < 1 || s->max_q > s->tq ? s->tq : s->max_q) : s->tq / s->batch;
+  const int64_t later = most - kBlock - (int64_t)d->left;
+  if (later < 2 * kFar) return 0;
+  // some 2048 work-groups in all: more would only add sums to store
+  return (int)std::min<int64_t>((later + kFar - 1) / kFar, std::max<int64_t>(1, 2048 / ((int64_t)s->batch * d->kv_heads)));
+}
+size_t far_bytes(const ttc_attn_desc* d, const ttc_attn_seqs* s) {
+  const int far = far_of(d, s);
+  return far == 0 ? 0 : (size_t)s->batch * d->kv_heads * (1 + far) * 2 * d->sinks * d->dim * sizeof(float);
 }
 
 // two buffers of two tiles
@@ -1062,9 +1139,9 @@ unsigned grid_of(AttnArgs& a, int64_t longest, int64_t t, int rows, int heads) {
   const int64_t most = a.q_off ? (longest < 1 || longest > t ? t : longest) : t / a.batch;
   int64_t tiles = (most + rows - 1) / rows;
   const int64_t cap = kMaxGroups / ((int64_t)a.batch * heads);
-  tiles = tiles < 1 ? 1 : tiles > cap ? cap : tiles;
+  tiles = std::max<int64_t>(1, std::min(tiles, cap));
   a.tiles = (int)tiles;
-  return (unsigned)(tiles * a.batch * heads);
+  return (unsigned)((tiles + a.far) * a.batch * heads);
 }
 
 ttc_status launched() { return hipGetLastError() == hipSuccess ? TTC_OK : TTC_ERR_HIP; }
@@ -1080,7 +1157,7 @@ extern "C" ttc_status ttc_attn_workspace(const ttc_attn_desc* desc, const ttc_at
   const ttc_status st = check_seqs(desc, seqs);
   if (st != TTC_OK) return st;
   *saved_bytes = stat_bytes(desc, seqs);
-  *scratch_bytes = stat_bytes(desc, seqs);
+  *scratch_bytes = stat_bytes(desc, seqs) + far_bytes(desc, seqs);
   return TTC_OK;
 }
 
@@ -1116,10 +1193,11 @@ extern "C" ttc_status ttc_attn_bwd(const ttc_attn_desc* desc, const ttc_attn_seq
                                    size_t scratch_bytes, ttc_stream_t stream) {
   const ttc_status st = check_seqs(desc, seqs);
   if (st != TTC_OK) return st;
+  const size_t scratch_need = stat_bytes(desc, seqs) + far_bytes(desc, seqs);
   if (seqs->tq > 0) {
     if (!q || !o || !d_o || !saved || !dq || !scratch) return TTC_ERR_NULL;
     if (!al16(q) || !al16(o) || !al16(d_o) || !al16(saved) || !al16(dq) || !al16(scratch)) return TTC_ERR_ALIGN;
-    if (saved_bytes < stat_bytes(desc, seqs) || scratch_bytes < stat_bytes(desc, seqs)) return TTC_ERR_WORKSPACE;
+    if (saved_bytes < stat_bytes(desc, seqs) || scratch_bytes < scratch_need) return TTC_ERR_WORKSPACE;
   }
   if (seqs->tk > 0) {
     if (!k || !v || !dk || !dv) return TTC_ERR_NULL;
@@ -1149,6 +1227,8 @@ extern "C" ttc_status ttc_attn_bwd(const ttc_attn_desc* desc, const ttc_attn_seq
     });
   }
   if (a.tk > 0) {
+    a.far = a.tq > 0 ? far_of(desc, seqs) : 0;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + stat_bytes(desc, seqs));
     const unsigned grid = grid_of(a, seqs->max_k, a.tk, kBlock, a.kv_heads);
     TraceScope ts("attn_dkv", s);
     with_geo(desc, [&](auto ty, auto ns) {
@@ -1156,6 +1236,11 @@ extern "C" ttc_status ttc_attn_bwd(const ttc_attn_desc* desc, const ttc_attn_seq
       constexpr int NS = decltype(ns)::value;
       launch(k_attn_dkv<T, NS>, grid, tile_lds<T, NS>(), s, a);
     });
+  }
+  if (a.far > 0) {
+    TraceScope ts("attn_sinks", s);
+    auto kern = desc->dtype == TTC_F32 ? k_attn_sinks<float> : k_attn_sinks<bf16_t>;
+    TTC_LAUNCH(kern, dim3((unsigned)(a.batch * a.kv_heads)), dim3(kThreads), 0, s, a);
   }
   return launched();
 }

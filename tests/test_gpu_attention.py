@@ -431,3 +431,36 @@ def test_refusals():
     with pytest.raises(ttc.TTCError) as e:
         layer.forward(z(60, 256), z(60, 128), z(60, 128), saved=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     assert e.value.code == 6
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("h,hk", [(1, 1), (4, 2)])
+@pytest.mark.parametrize("left,right,sinks", [(30, 0, 4), (100, 20, 33), (0, 0, 128), (64, -1, 1), (10, 5, 129)])
+def test_sinks_of_long_sequences(ty, h, hk, left, right, sinks):
+    """Many queries past the window of the first keys, which still see the sinks."""
+    _check([2300], [2300], h=h, hk=hk, d=32, window=(left, right), sinks=sinks, ty=ty, seed=sinks)
+    lens = [1900, 5, 0, 1400, 700]
+    _check(lens, [1900, 5, 40, 1500, 300], h=h, hk=hk, d=32, window=(left, right), sinks=sinks, ty=ty, seed=sinks, max_q=1900)
+
+
+@pytest.mark.parametrize("which", ["q", "do", "k", "v"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_sinks_of_long_sequences_see_bad_rows(which, bad):
+    """A bad row far behind the window: it reaches the sinks and, of the other keys, those in its window alone."""
+    ttc = _ttc()
+    n, d, window, sinks = 2300, 32, (30, 0), 4
+    layer = ttc.WindowAttention(1, d, window=window, sinks=sinks, dtype=F32)
+    t = dict(zip(("q", "k", "v", "do"), _inputs([n], [n], 1, 1, d, F32, 8)))
+    m = _seen(n, n, *window, sinks, "cuda")
+    cut = lambda x: x.view(n, 1, d)  # noqa: E731
+    ref = _reference(*map(cut, (t["q"], t["k"], t["v"], t["do"])), m, layer.desc.scale, E32, 1)
+    row = 2000
+    t[which][row] = bad
+    o, saved = layer.forward(t["q"], t["k"], t["v"])
+    got = (o,) + layer.backward(t["q"], t["k"], t["v"], o, t["do"], saved)
+    hit_q = m[:, row] if which in ("k", "v") else torch.arange(n, device="cuda") == row
+    hit_k = m[hit_q].any(0) | (torch.arange(n, device="cuda") == row)
+    for name, x, (y, bound), hit in zip(("o", "dq", "dk", "dv"), got, ref, (hit_q, hit_q, hit_k, hit_k)):
+        _close(cut(x)[~hit], y[~hit], bound[~hit], name)
+    if which in ("q", "do"):
+        assert not bool(torch.isfinite(got[2][:sinks]).all()), "the sinks are seen by the bad row"
