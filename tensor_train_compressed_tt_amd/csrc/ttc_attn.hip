@@ -44,6 +44,7 @@ struct AttnArgs {
   float* lse;
   float* delta;
   int64_t tq, tk;
+  int len_q, len_k;  // without offsets: rows of every sequence
   int batch, heads, kv_heads, dim;
   int left, right, sinks;
   float scale, scale2;  // scale2 = scale log2 e
@@ -58,11 +59,8 @@ struct Span {
   int64_t start;
   int len;
 };
-__device__ __forceinline__ Span span_of(const int32_t* off, int b, int batch, int64_t t) {
-  if (!off) {
-    const int len = (int)(t / batch);
-    return {(int64_t)b * len, len};
-  }
+__device__ __forceinline__ Span span_of(const int32_t* off, int b, int len, int64_t t) {
+  if (!off) return {(int64_t)b * len, len};
   const int64_t s = min(max((int64_t)off[b], (int64_t)0), t), e = min(max((int64_t)off[b + 1], s), t);
   return {s, (int)(e - s)};
 }
@@ -446,21 +444,58 @@ __device__ __forceinline__ bool none_seen(const AttnArgs& a, int j, int n, int p
 __device__ __forceinline__ bool all_seen(const AttnArgs& a, int j, int n, int p0, int p1, int lk) {
   return j + n <= lk && j + n - 1 <= p0 + a.right && (j >= p1 - a.left || j + n <= a.sinks);
 }
-__device__ __forceinline__ bool seen(const AttnArgs& a, int j, int p, int lk) {
-  return j < lk && j <= p + a.right && (j >= p - a.left || j < a.sinks);
+// A lane's view of the 32 rows of the other side that its results stand for:
+// those of numbers [lo, lo + span) or, as sinks, below `keep` are seen.  One
+// comparison a result where no sinks are among them.
+struct View {
+  uint32_t at, span;  // row 0's place in the window, the window's length
+  int row, keep;
+  // results of rows first + 8 (i / 4) + 4 g + i % 4, rows [lo, hi) seen, those below sinks too
+  __device__ __forceinline__ View(int first, int lo, int hi, int sinks) {
+    row = first + 4 * ((threadIdx.x >> 5) & 1);
+    at = (uint32_t)(row - lo);
+    span = (uint32_t)max(0, hi - lo);
+    keep = sinks;
+  }
+  template <bool SINKS>
+  __device__ __forceinline__ bool operator()(int i) const {
+    const int d = 8 * (i / 4) + i % 4;
+    return at + d < span || (SINKS && row + d < keep);
+  }
+  // v[i] where seen, else `none`
+  __device__ __forceinline__ void cut(f32x16& v, float none) const {
+    if (__ballot(row < keep) == 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = operator()<false>(i) ? v[i] : none;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = operator()<true>(i) ? v[i] : none;
+    }
+  }
+};
+// of keys, by the query at place p
+__device__ __forceinline__ View key_view(const AttnArgs& a, int j, int p, int lk) {
+  const int hi = min(lk, p + a.right + 1);
+  return View(j, p - a.left, hi, min(a.sinks, hi));
+}
+
+// work-groups of k_attn_fwd and k_attn_dq that a CU holds, as a wave's registers allow
+template <typename T, int NS>
+constexpr int key_groups() {
+  return sizeof(typename Elem<T>::type) == 2 ? (NS <= 2 ? 3 : 2) : NS <= 2 ? 2 : 1;
 }
 
 constexpr float kSlack = 8.f;  // P stays below 2^8 times its largest: far from overflow in fp32 and bf16
 
 template <typename T, int NS>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_fwd(AttnArgs a) {
   typedef Geo<T, NS> G;
   typedef typename G::E E;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   E* const tiles = reinterpret_cast<E*>(lds_raw);
   constexpr int TS = kTile * G::LD;
   const Place w = place_of(a, a.heads);
-  const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
+  const Span sq = span_of(a.q_off, w.b, a.len_q, a.tq), sk = span_of(a.k_off, w.b, a.len_k, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
   const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
   const int hk = w.head / (a.heads / a.kv_heads), lk = sk.len, shift = sk.len - sq.len;
@@ -506,10 +541,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(AttnArgs a) {
         for (int h = 0; h < 2; ++h) s[h] = rows_times_own<T, NS>(tk, h, qf);
         if (!all_seen(a, j0, kTile, p0, p1, lk)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              s[h][i] = seen(a, j0 + 32 * h + 8 * (i / 4) + 4 * g + i % 4, p, lk) ? s[h][i] : -INFINITY;
+          for (int h = 0; h < 2; ++h) key_view(a, j0 + 32 * h, p, lk).cut(s[h], -INFINITY);
         }
         float top = s[0][0];
 #pragma unroll
@@ -563,14 +595,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_fwd(AttnArgs a) {
 
 // dq, and delta for k_attn_dkv
 template <typename T, int NS>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_dq(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(AttnArgs a) {
   typedef Geo<T, NS> G;
   typedef typename G::E E;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   E* const tiles = reinterpret_cast<E*>(lds_raw);
   constexpr int TS = kTile * G::LD;
   const Place w = place_of(a, a.heads);
-  const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
+  const Span sq = span_of(a.q_off, w.b, a.len_q, a.tq), sk = span_of(a.k_off, w.b, a.len_k, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
   const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
   const int hk = w.head / (a.heads / a.kv_heads), lk = sk.len, shift = sk.len - sq.len;
@@ -629,17 +661,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_dq(AttnArgs a) {
         if (rows <= 0 || none_seen(a, j, 32, p0, p1, lk)) continue;
         f32x16 s = rows_times_own<T, NS>(tk, h, qf);
         const f32x16 dp = rows_times_own<T, NS>(tv, h, of);
-        if (all_seen(a, j, 32, p0, p1, lk)) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * (dp[i] - dl);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[i] = seen(a, j + 8 * (i / 4) + 4 * g + i % 4, p, lk)
-                       ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * (dp[i] - dl)
-                       : 0.f;
-        }
+        for (int i = 0; i < 16; ++i)
+          s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * (dp[i] - dl);
+        if (!all_seen(a, j, 32, p0, p1, lk)) key_view(a, j, p, lk).cut(s, 0.f);
         cols_times_result<T, NS>(tk, h, s, acc);
       }
       if (nx < kt.hi) {
@@ -683,7 +708,7 @@ __global__ __launch_bounds__(kThreads, (dkv_groups<T, NS>())) void k_attn_dkv(At
   E* const tiles = reinterpret_cast<E*>(lds_raw);
   constexpr int TS = kTile * G::LD, kPiece = kFar / kTile;
   const Place w = place_of(a, a.kv_heads);
-  const Span sq = span_of(a.q_off, w.b, a.batch, a.tq), sk = span_of(a.k_off, w.b, a.batch, a.tk);
+  const Span sq = span_of(a.q_off, w.b, a.len_q, a.tq), sk = span_of(a.k_off, w.b, a.len_k, a.tk);
   const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
   const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
   const int group = a.heads / a.kv_heads, lq = sq.len, lk = sk.len, shift = sk.len - sq.len;
@@ -769,14 +794,10 @@ __global__ __launch_bounds__(kThreads, (dkv_groups<T, NS>())) void k_attn_dkv(At
             dp[z] = s[z] * (dp[z] - d4[e]);
           }
         }
-        if (!whole) {
-#pragma unroll
-          for (int z = 0; z < 16; ++z) {
-            const int r = i + 8 * (z / 4) + 4 * g + z % 4;
-            const bool on = r < lq && seen(a, j, r + shift, lk);
-            s[z] = on ? s[z] : 0.f;
-            dp[z] = on ? dp[z] : 0.f;
-          }
+        if (!whole) {  // queries that see key j: from j - right on, to j + left or, of a sink, to the end
+          const View see(i, max(0, j - a.right - shift), j < a.sinks ? lq : min(lq, j + a.left - shift + 1), 0);
+          see.cut(s, 0.f);
+          see.cut(dp, 0.f);
         }
         cols_times_result<T, NS>(td, hf, s, av);
         cols_times_result<T, NS>(tq, hf, dp, ak);
@@ -833,7 +854,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void k_attn_sinks(AttnArgs a) {
   typedef typename Elem<T>::type E;
   const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
-  const Span sk = span_of(a.k_off, b, a.batch, a.tk);
+  const Span sk = span_of(a.k_off, b, a.len_k, a.tk);
   const int64_t ldk = (int64_t)a.kv_heads * a.dim, unit = (int64_t)2 * a.sinks * a.dim;
   const float* part = a.part + (int64_t)blockIdx.x * (1 + a.far) * unit;
   const int n = min(a.sinks, sk.len) * a.dim;
@@ -1129,6 +1150,8 @@ AttnArgs make_args(const ttc_attn_desc* d, const ttc_attn_seqs* s) {
   a.tq = s->tq;
   a.tk = s->tk;
   a.batch = s->batch;
+  a.len_q = (int)(s->tq / s->batch);
+  a.len_k = (int)(s->tk / s->batch);
   return a;
 }
 
