@@ -91,6 +91,15 @@ __device__ __forceinline__ float dot_row(const typename Elem<T>::type* a, const 
   return s;
 }
 
+// what a row's keys and scores depend on
+struct Mask {
+  int left, right, sinks, dim;
+  float scale, scale2;
+};
+__device__ __forceinline__ Mask mask_of(const AttnArgs& a) {
+  return {a.left, a.right, a.sinks, a.dim, a.scale, a.scale2};
+}
+
 // A row at a time, by one wave: the lanes take 64 keys (or queries) for the
 // scores, then two of the row's elements each for the products.  Only rows
 // that are seen are ever multiplied, so a NaN or an infinity that a row does
@@ -98,7 +107,7 @@ __device__ __forceinline__ float dot_row(const typename Elem<T>::type* a, const 
 
 // o of one query at place p: acc[e] is element lane + 64 e
 template <typename T>
-__device__ void row_fwd(const AttnArgs& a, const typename Elem<T>::type* q, const typename Elem<T>::type* k,
+__device__ __noinline__ void row_fwd(Mask a, const typename Elem<T>::type* q, const typename Elem<T>::type* k,
                         const typename Elem<T>::type* v, int64_t ldk, int p, int lk, float (&acc)[2], float& lse) {
   const int lane = threadIdx.x & 63;
   float m = -INFINITY, l = 0.f;
@@ -140,7 +149,7 @@ __device__ __forceinline__ void row_store(typename Elem<T>::type* o, const float
 
 // dq of one query at place p
 template <typename T>
-__device__ void row_dq(const AttnArgs& a, const typename Elem<T>::type* q, const typename Elem<T>::type* d_o,
+__device__ __noinline__ void row_dq(Mask a, const typename Elem<T>::type* q, const typename Elem<T>::type* d_o,
                        const typename Elem<T>::type* k, const typename Elem<T>::type* v, int64_t ldk, int p, int lk,
                        float lse, float delta, float (&acc)[2]) {
   const int lane = threadIdx.x & 63;
@@ -168,7 +177,7 @@ __device__ void row_dq(const AttnArgs& a, const typename Elem<T>::type* q, const
 // what queries [i0, i_end) of one query head add to dk and dv of key j, which
 // all of them see; q, d_o, lse, delta from the sequence's first row on
 template <typename T>
-__device__ void row_dkv(const AttnArgs& a, const typename Elem<T>::type* q, const typename Elem<T>::type* d_o,
+__device__ __noinline__ void row_dkv(Mask a, const typename Elem<T>::type* q, const typename Elem<T>::type* d_o,
                         const float* lse, const float* delta, int64_t ldq, const typename Elem<T>::type* k,
                         const typename Elem<T>::type* v, int i0, int i_end, float (&dk)[2], float (&dv)[2]) {
   const int lane = threadIdx.x & 63;
@@ -586,7 +595,7 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_fwd(At
     for (uint32_t left = bad; left; left &= left - 1) {
       const int i = q0 + __builtin_ctz(left);
       float r[2], stat;
-      row_fwd<T>(a, q + (int64_t)i * ldq, k, v, ldk, i + shift, lk, r, stat);
+      row_fwd<T>(mask_of(a), q + (int64_t)i * ldq, k, v, ldk, i + shift, lk, r, stat);
       row_store<T>(o + (int64_t)i * ldq, r, a.dim);
       if ((threadIdx.x & 63) == 0) lse[i] = stat;
     }
@@ -679,7 +688,7 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(Att
     for (uint32_t left = bad; left; left &= left - 1) {
       const int n = __builtin_ctz(left), i = q0 + n;
       float r[2];
-      row_dq<T>(a, q + (int64_t)i * ldq, d_o + (int64_t)i * ldq, k, v, ldk, i + shift, lk, lane_value(sub, n),
+      row_dq<T>(mask_of(a), q + (int64_t)i * ldq, d_o + (int64_t)i * ldq, k, v, ldk, i + shift, lk, lane_value(sub, n),
                 lane_value(dl, n), r);
       row_store<T>(dq + (int64_t)i * ldq, r, a.dim);
     }
@@ -828,7 +837,7 @@ __global__ __launch_bounds__(kThreads, (dkv_groups<T, NS>())) void k_attn_dkv(At
       const int y0 = max(0, y - a.right - shift), y1 = y < a.sinks ? lq : min(lq, y + a.left - shift + 1);
       for (int hh = 0; hh < group; ++hh) {
         const auto add = [&](int from, int to) {
-          row_dkv<T>(a, q + hh * a.dim, d_o + hh * a.dim, lse + (int64_t)hh * a.tq, delta + (int64_t)hh * a.tq, ldq,
+          row_dkv<T>(mask_of(a), q + hh * a.dim, d_o + hh * a.dim, lse + (int64_t)hh * a.tq, delta + (int64_t)hh * a.tq, ldq,
                      k + (int64_t)y * ldk, v + (int64_t)y * ldk, from, to, rk, rv);
         };
         if (!far)
