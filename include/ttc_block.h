@@ -181,7 +181,7 @@ typedef struct {
   int32_t steps;    /* 1 .. 32              */
   int32_t nesterov; /* look-ahead: 0 or 1   */
   float a, b, c;    /* finite               */
-  float eps;        /* > 0                  */
+  float eps;        /* normal, > 0          */
   float lr, mu, weight_decay;
 } ttc_ortho_desc;
 

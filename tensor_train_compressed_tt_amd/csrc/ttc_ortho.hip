@@ -16,6 +16,7 @@
 // CU's LDS and no launch of its own, and the work-groups of a step, which are
 // in different phases, share memory and matrix units.
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -30,8 +31,6 @@ namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxSide = 128;
 constexpr int kMaxSteps = 32;
 constexpr int kLdsSide = 64;  // the S x S matrices of larger ones lie in the scratch
@@ -56,8 +55,20 @@ struct OrthoArgs {
   int steps, ahead;
 };
 
-constexpr int ld_of(int sp) { return sp + 2; }
-constexpr int mat_size(int sp) { return sp * ld_of(sp); }
+// The S x S matrices are symmetric: the 16 x 16 tiles on and above the diagonal
+// are kept, row by row, so that three of 64 x 64 leave room for two
+// work-groups on a CU (69 of 160 KB).  Rows of a tile start two doubles
+// further than they are long: in other banks.
+constexpr int kTileLd = 18;
+constexpr int kTileSize = 16 * kTileLd;
+constexpr int tiles_of(int nt) { return nt * (nt + 1) / 2; }
+constexpr int mat_size(int nt) { return tiles_of(nt) * kTileSize; }
+__device__ __forceinline__ int tile_at(int p, int q, int nt) { return (p * nt - p * (p - 1) / 2 + q - p) * kTileSize; }
+__device__ __forceinline__ double sym_at(const double* x, int row, int col, int nt) {
+  const int p = row >> 4, q = col >> 4;
+  return p <= q ? x[tile_at(p, q, nt) + (row & 15) * kTileLd + (col & 15)]
+                : x[tile_at(q, p, nt) + (col & 15) * kTileLd + (row & 15)];
+}
 
 // One k-step of four: lane l holds row l % 16 of A and column l % 16 of B at
 // k = l / 16; element r of the result is row 4 r + l / 16, column l % 16.
@@ -65,23 +76,49 @@ __device__ __forceinline__ f64x4 mma64(double x, double y, f64x4 c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(x, y, c, 0, 0, 0);
 }
 
-// N elements of u of one row of the long side; FIRST also steps the momentum
-template <int N, bool FIRST>
-__device__ __forceinline__ void load_u(const OrthoArgs& a, const Mat& t, int64_t i, int j, float (&u)[N]) {
+// N neighbouring elements (i, j ..) as one load or store (VEC) or single ones.
+// Elements outside the matrix are read as its last ones, with no branch, and
+// not written.
+template <int N, bool VEC>
+__device__ __forceinline__ void load_n(const float* base, const Mat& t, int64_t i, int j, float (&v)[N]) {
+  i = min(i, t.len - 1);
+  if constexpr (VEC) {
+    typedef float vec __attribute__((ext_vector_type(N)));
+    const vec x = *reinterpret_cast<const vec*>(base + i * t.si + min(j, t.side - N));
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    u[e] = 0.f;
-    if (i < t.len && j + e < t.side) {
-      const int64_t at = i * t.si + (j + e) * t.sj;
-      const float g = t.g[at];
-      float m = t.m[at];
-      if (FIRST) {
-        m = a.mu * m + g;
-        t.m[at] = m;
-      }
-      u[e] = a.ahead ? g + a.mu * m : m;
-    }
+    for (int e = 0; e < N; ++e) v[e] = x[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = base[i * t.si + min(j + e, t.side - 1) * t.sj];
   }
+}
+template <int N, bool VEC>
+__device__ __forceinline__ void store_n(float* base, const Mat& t, int64_t i, int j, const float (&v)[N]) {
+  if (i >= t.len) return;
+  if constexpr (VEC) {
+    typedef float vec __attribute__((ext_vector_type(N)));
+    vec x;
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = v[e];
+    if (j < t.side) *reinterpret_cast<vec*>(base + i * t.si + j) = x;
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (j + e < t.side) base[i * t.si + (j + e) * t.sj] = v[e];
+  }
+}
+// rows of `n` neighbouring elements that can be read at once
+__device__ __forceinline__ bool vectors(const Mat& t, int n) {
+  const uintptr_t all = (uintptr_t)t.w | (uintptr_t)t.g | (uintptr_t)t.m;
+  return t.sj == 1 && t.side % n == 0 && all % (4 * n) == 0;
+}
+
+// U rows of N elements of u from what was loaded; zeros outside the matrix
+template <int N>
+__device__ __forceinline__ void make_u(const OrthoArgs& a, const Mat& t, int64_t i, int j, const float (&g)[N],
+                                       const float (&m)[N], float (&u)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) u[e] = i < t.len && j + e < t.side ? (a.ahead ? g[e] + a.mu * m[e] : m[e]) : 0.f;
 }
 
 // Place of column j in the order that the S x S matrices are kept in: a lane
@@ -91,46 +128,76 @@ __device__ __forceinline__ int place(int j, int nt) {
   return blk * 16 * nt + (r % nt) * 16 + r / nt;
 }
 
-// out (NT * 16 square, places) = sum over rows of u[block bi]^T u[block bj], all
-// tiles of an off-diagonal block, those on and above the diagonal of a diagonal
-// one, written to both sides.  Each wave sums its own rows; the waves' sums are
-// added in a fixed order through `lds`.
-template <int NT, bool DIAG>
-__device__ void gram(const OrthoArgs& a, const Mat& t, int bi, int bj, double* lds, double* out, int ld) {
-  constexpr int TILES = DIAG ? NT * (NT + 1) / 2 : NT * NT;
+constexpr int kSumTiles = 4;  // tiles of a wave that are summed over the waves at once
+
+// out = sum over rows of u[block bi]^T u[block bj], all tiles of an off-diagonal
+// block, those on and above the diagonal of a diagonal one.  Diagonal blocks
+// also step the momentum.  Each wave sums its own rows, ROWS x 4 of them in
+// flight; the waves' sums are added in a fixed order through `lds`.
+template <int WAVES, int NT, bool DIAG, bool VEC>
+__device__ void gram(const OrthoArgs& a, const Mat& t, int bi, int bj, double* lds, double* out, int nt) {
+  constexpr int TILES = DIAG ? tiles_of(NT) : NT * NT;
+  constexpr int ROWS = NT == 1 ? 8 : NT == 2 ? 4 : DIAG ? 2 : 1;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  const int ji = bi * 16 * NT + c * NT, jj = bj * 16 * NT + c * NT;
   f64x4 acc[TILES];
 #pragma unroll
   for (int x = 0; x < TILES; ++x) acc[x] = f64x4{0., 0., 0., 0.};
-  for (int64_t i0 = 4 * w; i0 < t.len; i0 += 4 * kWaves) {
-    float ui[NT], uj[NT];
-    load_u<NT, DIAG>(a, t, i0 + g, bi * 16 * NT + c * NT, ui);
-    if (!DIAG) load_u<NT, false>(a, t, i0 + g, bj * 16 * NT + c * NT, uj);
-    double di[NT], dj[NT];
+  for (int64_t i0 = 4 * ROWS * w; i0 < t.len; i0 += 4 * ROWS * WAVES) {
+    float gi[ROWS][NT], mi[ROWS][NT], gj[DIAG ? 1 : ROWS][NT], mj[DIAG ? 1 : ROWS][NT];
 #pragma unroll
-    for (int e = 0; e < NT; ++e) {
-      di[e] = ui[e];
-      dj[e] = DIAG ? ui[e] : uj[e];
+    for (int r = 0; r < ROWS; ++r) {
+      load_n<NT, VEC>(t.g, t, i0 + 4 * r + g, ji, gi[r]);
+      load_n<NT, VEC>(t.m, t, i0 + 4 * r + g, ji, mi[r]);
+      if constexpr (!DIAG) {
+        load_n<NT, VEC>(t.g, t, i0 + 4 * r + g, jj, gj[r]);
+        load_n<NT, VEC>(t.m, t, i0 + 4 * r + g, jj, mj[r]);
+      }
     }
-    int x = 0;
 #pragma unroll
-    for (int p = 0; p < NT; ++p)
+    for (int r = 0; r < ROWS; ++r) {
+      const int64_t i = i0 + 4 * r + g;
+      if constexpr (DIAG) {
 #pragma unroll
-      for (int q = DIAG ? p : 0; q < NT; ++q, ++x) acc[x] = mma64(di[p], dj[q], acc[x]);
+        for (int e = 0; e < NT; ++e) mi[r][e] = a.mu * mi[r][e] + gi[r][e];
+        store_n<NT, VEC>(t.m, t, i, ji, mi[r]);
+      }
+      float ui[NT], uj[NT];
+      make_u<NT>(a, t, i, ji, gi[r], mi[r], ui);
+      if constexpr (!DIAG) make_u<NT>(a, t, i, jj, gj[r], mj[r], uj);
+      double di[NT], dj[NT];
+#pragma unroll
+      for (int e = 0; e < NT; ++e) {
+        di[e] = ui[e];
+        dj[e] = DIAG ? ui[e] : uj[e];
+      }
+      int x = 0;
+#pragma unroll
+      for (int p = 0; p < NT; ++p)
+#pragma unroll
+        for (int q = DIAG ? p : 0; q < NT; ++q, ++x) acc[x] = mma64(di[p], dj[q], acc[x]);
+    }
   }
-  for (int half = kWaves / 2; half > 0; half >>= 1) {
-    __syncthreads();
-    if (w >= half && w < 2 * half)
 #pragma unroll
-      for (int x = 0; x < TILES; ++x)
+  for (int x0 = 0; x0 < TILES; x0 += kSumTiles) {
+    constexpr int N = TILES < kSumTiles ? TILES : kSumTiles;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) lds[(((w - half) * TILES + x) * 4 + r) * 64 + lane] = acc[x][r];
-    __syncthreads();
-    if (w < half)
+    for (int half = WAVES / 2; half > 0; half >>= 1) {
+      __syncthreads();
+      if (w >= half && w < 2 * half)
 #pragma unroll
-      for (int x = 0; x < TILES; ++x)
+        for (int x = 0; x < N; ++x)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[x][r] += lds[((w * TILES + x) * 4 + r) * 64 + lane];
+          for (int r = 0; r < 4; ++r)
+            if (x0 + x < TILES) lds[(((w - half) * N + x) * 4 + r) * 64 + lane] = acc[x0 + x < TILES ? x0 + x : 0][r];
+      __syncthreads();
+      if (w < half)
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (x0 + x < TILES) acc[x0 + x < TILES ? x0 + x : 0][r] += lds[((w * N + x) * 4 + r) * 64 + lane];
+    }
   }
   __syncthreads();  // `out` may be what the sums went through
   if (w == 0) {
@@ -140,13 +207,17 @@ __device__ void gram(const OrthoArgs& a, const Mat& t, int bi, int bj, double* l
 #pragma unroll
       for (int q = DIAG ? p : 0; q < NT; ++q, ++x)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = (bi * NT + p) * 16 + 4 * r + g, col = (bj * NT + q) * 16 + c;
-          out[row * ld + col] = acc[x][r];
-          out[col * ld + row] = acc[x][r];
-        }
+        for (int r = 0; r < 4; ++r) out[tile_at(bi * NT + p, bj * NT + q, nt) + (4 * r + g) * kTileLd + c] = acc[x][r];
   }
   __syncthreads();
+}
+
+template <int WAVES, int NT, bool DIAG>
+__device__ __forceinline__ void gram(const OrthoArgs& a, const Mat& t, int bi, int bj, double* lds, double* out, int nt) {
+  if (NT != 3 && vectors(t, NT))
+    gram<WAVES, NT, DIAG, NT != 3>(a, t, bi, bj, lds, out, nt);
+  else
+    gram<WAVES, NT, DIAG, false>(a, t, bi, bj, lds, out, nt);
 }
 
 // Tile x of the nt (nt + 1) / 2 tiles on and above the diagonal.
@@ -157,160 +228,183 @@ __device__ __forceinline__ void tile_of(int x, int nt, int& p, int& q) {
 }
 
 // Tile (p, q) of the product of two symmetric matrices that commute
-__device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, int p, int q, int sp, int ld) {
-  const int lane = threadIdx.x & 63;
-  const double* rx = x + (p * 16 + (lane & 15)) * ld + (lane >> 4);
-  const double* ry = y + (q * 16 + (lane & 15)) * ld + (lane >> 4);
+__device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, int p, int q, int nt) {
+  const int lane = threadIdx.x & 63, along = (lane & 15) * kTileLd + (lane >> 4), across = (lane >> 4) * kTileLd + (lane & 15);
   f64x4 acc = {0., 0., 0., 0.};
-#pragma unroll 4
-  for (int k = 0; k < sp; k += 4) acc = mma64(rx[k], ry[k], acc);
+#pragma unroll 1
+  for (int b = 0; b < nt; ++b) {  // rows p and q of the tiles' column b, or of row b turned over
+    const double* rx = x + (b >= p ? tile_at(p, b, nt) + along : tile_at(b, p, nt) + across);
+    const double* ry = y + (b >= q ? tile_at(q, b, nt) + along : tile_at(b, q, nt) + across);
+    const int sx = b >= p ? 4 : 4 * kTileLd, sy = b >= q ? 4 : 4 * kTileLd;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc = mma64(rx[k * sx], ry[k * sy], acc);
+  }
   return acc;
 }
 
-template <typename F>
-__device__ __forceinline__ void each_of_tile(int p, int q, int ld, F f) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = p * 16 + 4 * r + (lane >> 4), col = q * 16 + (lane & 15);
-    f(r, row, col, row * ld + col, col * ld + row);
-  }
-}
-
-// mats in LDS: at most two tiles a wave (10 tiles of 8 waves); in the scratch 5
-constexpr int kTilesPerWave = 5;
-
-// A_0 in `A` -> Q in `Q`, over n steps; P is the third matrix
+// A_0 in `A` -> Q in `Q`, over n steps; P is the third matrix.  A wave has at
+// most TPW tiles.
+template <int WAVES, int TPW>
 __device__ void iterate(const OrthoArgs& a, double* A, double* P, double* Q, int nt) {
-  const int w = threadIdx.x >> 6, sp = nt * 16, ld = ld_of(sp), tiles = nt * (nt + 1) / 2;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, tiles = tiles_of(nt);
+  const int mine = (lane >> 4) * kTileLd + (lane & 15);  // element r of a result: 4 r rows further
+  int p[TPW], q[TPW], at[TPW];
+#pragma unroll
+  for (int y = 0; y < TPW; ++y) {
+    tile_of(min(w + y * WAVES, tiles - 1), nt, p[y], q[y]);
+    at[y] = tile_at(p[y], q[y], nt) + mine;
+  }
   for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
-    for (int x = w; x < tiles; x += kWaves) {
-      int p, q;
-      tile_of(x, nt, p, q);
-      const f64x4 s = tile_product(A, A, p, q, sp, ld);
-      each_of_tile(p, q, ld, [&](int r, int row, int col, int at, int mirror) {
-        const double v = (row == col ? a.a : 0.) + a.b * A[at] + a.c * s[r];
-        P[at] = v;
-        P[mirror] = v;
-        if (k == 0) {
-          Q[at] = v;
-          Q[mirror] = v;
-        }
-      });
+#pragma unroll
+    for (int y = 0; y < TPW; ++y) {
+      if (w + y * WAVES >= tiles) break;
+      const f64x4 s = tile_product(A, A, p[y], q[y], nt);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int x = at[y] + 4 * r * kTileLd;
+        const double v = (p[y] == q[y] && 4 * r + (lane >> 4) == (lane & 15) ? a.a : 0.) + a.b * A[x] + a.c * s[r];
+        P[x] = v;
+        if (k == 0) Q[x] = v;
+      }
     }
     __syncthreads();
-    f64x4 fa[kTilesPerWave], fq[kTilesPerWave];
+    if (last && k == 0) break;
+    f64x4 fa[TPW], fq[TPW];
 #pragma unroll
-    for (int y = 0; y < kTilesPerWave; ++y) {
-      const int x = w + y * kWaves;
-      if (x >= tiles) break;
-      int p, q;
-      tile_of(x, nt, p, q);
-      if (!last) fa[y] = tile_product(A, P, p, q, sp, ld);
-      if (k > 0) fq[y] = tile_product(Q, P, p, q, sp, ld);
+    for (int y = 0; y < TPW; ++y) {
+      if (w + y * WAVES >= tiles) break;
+      if (!last) fa[y] = tile_product(A, P, p[y], q[y], nt);
+      if (k > 0) fq[y] = tile_product(Q, P, p[y], q[y], nt);
     }
     __syncthreads();
 #pragma unroll
-    for (int y = 0; y < kTilesPerWave; ++y) {
-      const int x = w + y * kWaves;
-      if (x >= tiles) break;
-      int p, q;
-      tile_of(x, nt, p, q);
-      each_of_tile(p, q, ld, [&](int r, int, int, int at, int mirror) {
-        if (!last) A[at] = A[mirror] = fa[y][r];
-        if (k > 0) Q[at] = Q[mirror] = fq[y][r];
-      });
+    for (int y = 0; y < TPW; ++y) {
+      if (w + y * WAVES >= tiles) break;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int x = at[y] + 4 * r * kTileLd;
+        if (!last) A[x] = fa[y][r];
+        if (k > 0) Q[x] = fq[y][r];
+      }
     }
     __syncthreads();
     if (last) break;
 #pragma unroll
-    for (int y = 0; y < kTilesPerWave; ++y) {
-      const int x = w + y * kWaves;
-      if (x >= tiles) break;
-      int p, q;
-      tile_of(x, nt, p, q);
-      fa[y] = tile_product(A, P, p, q, sp, ld);
+    for (int y = 0; y < TPW; ++y) {
+      if (w + y * WAVES >= tiles) break;
+      fa[y] = tile_product(A, P, p[y], q[y], nt);
     }
     __syncthreads();
 #pragma unroll
-    for (int y = 0; y < kTilesPerWave; ++y) {
-      const int x = w + y * kWaves;
-      if (x >= tiles) break;
-      int p, q;
-      tile_of(x, nt, p, q);
-      each_of_tile(p, q, ld, [&](int r, int, int, int at, int mirror) { A[at] = A[mirror] = fa[y][r]; });
+    for (int y = 0; y < TPW; ++y) {
+      if (w + y * WAVES >= tiles) break;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) A[at[y] + 4 * r * kTileLd] = fa[y][r];
     }
     __syncthreads();
   }
 }
 
-__global__ __launch_bounds__(kThreads) void k_ortho(OrthoArgs a) {
-  extern __shared__ __attribute__((aligned(16))) double lds[];
-  const Mat t = a.mats[blockIdx.x];
-  const int S = t.side, nt = (S + 15) / 16, block = nt <= 4 ? nt : 4;  // tiles of a block of columns
-  const int all = nt <= 4 ? nt : 8, sp = all * 16, ld = ld_of(sp);
-  double* base = nt <= 4 ? lds : a.scratch + t.scratch;
-  double *A = base, *P = base + mat_size(sp), *Q = P + mat_size(sp);
-  if (nt == 1) {
-    gram<1, true>(a, t, 0, 0, lds, A, ld);
-  } else if (nt == 2) {
-    gram<2, true>(a, t, 0, 0, lds, A, ld);
-  } else if (nt == 3) {
-    gram<3, true>(a, t, 0, 0, lds, A, ld);
-  } else {
-    gram<4, true>(a, t, 0, 0, lds, A, ld);
-    if (nt > 4) {
-      gram<4, true>(a, t, 1, 1, lds, A, ld);
-      gram<4, false>(a, t, 0, 1, lds, A, ld);
+// w of all rows: 16 rows a wave, NT tiles of 16 columns.  qf: Q in fp32, rows of lq
+template <int WAVES, int NT, bool VEC>
+__device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const float step = a.lr * t.scale;
+  for (int64_t i0 = 16 * (threadIdx.x >> 6); i0 < t.len; i0 += 16 * WAVES) {
+    const int64_t i = i0 + c;
+    constexpr bool AHEAD = NT <= 4;  // w with g and m; of more tiles, one by one
+    float ug[NT][4], um[NT][4], w[AHEAD ? NT : 1][4];
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      load_n<4, VEC>(t.g, t, i, s * 16 + 4 * g, ug[s]);
+      load_n<4, VEC>(t.m, t, i, s * 16 + 4 * g, um[s]);
+      if constexpr (AHEAD) load_n<4, VEC>(t.w, t, i, s * 16 + 4 * g, w[s]);
+    }
+    f32x4 x[NT];
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      float u[4];
+      make_u<4>(a, t, i, s * 16 + 4 * g, ug[s], um[s], u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[s][e] = (float)(u[e] * inv);
+    }
+    const auto column = [&](int o, float (&to)[4]) {
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int s = 0; s < NT; ++s)
+        acc = Mma<float>::mma(*reinterpret_cast<const f32x4*>(qf + (o * 16 + c) * lq + s * 16 + 4 * g), x[s], acc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[e] = to[e] * a.decay - step * acc[e];
+      store_n<4, VEC>(t.w, t, i, o * 16 + 4 * g, to);
+    };
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int o = 0; o < NT; ++o) column(o, w[o]);
+    } else {
+#pragma unroll 1
+      for (int o = 0; o < NT; ++o) {
+        load_n<4, VEC>(t.w, t, i, o * 16 + 4 * g, w[0]);
+        column(o, w[0]);
+      }
     }
   }
+}
+template <int WAVES, int NT>
+__device__ __forceinline__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv) {
+  if (vectors(t, 4))
+    apply<WAVES, NT, true>(a, t, qf, lq, inv);
+  else
+    apply<WAVES, NT, false>(a, t, qf, lq, inv);
+}
+
+// BIG: a side over kLdsSide, whose S x S matrices lie in the scratch.  A SIMD
+// holds four waves (128 registers each), two where the 16 tiles of a block of
+// a large Gram matrix are summed.
+template <int WAVES, bool BIG>
+__global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) {
+  extern __shared__ __attribute__((aligned(16))) double lds[];
+  const Mat t = a.mats[blockIdx.x];
+  const int S = t.side, all = BIG ? kMaxSide / 16 : (S + 15) / 16, block = BIG ? 4 : all;  // tiles of a block of columns
+  double* base = BIG ? a.scratch + t.scratch : lds;
+  double *A = base, *P = base + mat_size(all), *Q = P + mat_size(all);
+  if constexpr (BIG) {
+    gram<WAVES, 4, true>(a, t, 0, 0, lds, A, all);
+    gram<WAVES, 4, true>(a, t, 1, 1, lds, A, all);
+    gram<WAVES, 4, false>(a, t, 0, 1, lds, A, all);
+  } else {
+    if (all == 1) gram<WAVES, 1, true>(a, t, 0, 0, lds, A, all);
+    else if (all == 2) gram<WAVES, 2, true>(a, t, 0, 0, lds, A, all);
+    else if (all == 3) gram<WAVES, 3, true>(a, t, 0, 0, lds, A, all);
+    else gram<WAVES, 4, true>(a, t, 0, 0, lds, A, all);
+  }
   double trace = 0.;
-  for (int j = 0; j < sp; ++j) trace += A[j * ld + j];
+#pragma unroll 4
+  for (int j = 0; j < 16 * all; ++j) trace += sym_at(A, j, j, all);
   // a NaN stays one: the comparison with it is false
   const double norm = sqrt(trace), inv = 1. / (norm < (double)a.eps ? (double)a.eps : norm);
   __syncthreads();
-  for (int x = threadIdx.x; x < mat_size(sp); x += kThreads) A[x] *= inv * inv;
+#pragma unroll 4
+  for (int x = threadIdx.x; x < mat_size(all); x += 64 * WAVES) A[x] *= inv * inv;
   __syncthreads();
-  iterate(a, A, P, Q, all);
+  iterate<WAVES, (tiles_of(BIG ? kMaxSide / 16 : kLdsSide / 16) + WAVES - 1) / WAVES>(a, A, P, Q, all);
 
   // Q in fp32, in the columns' own order, where A and P were
   float* qf = reinterpret_cast<float*>(A);
-  const int lq = sp + 4;
-  for (int x = threadIdx.x; x < sp * sp; x += kThreads) {
+  const int sp = 16 * all, lq = sp + 4;
+#pragma unroll 4
+  for (int x = threadIdx.x; x < sp * sp; x += 64 * WAVES) {
     const int r = x / sp, c = x - r * sp;
-    qf[r * lq + c] = (float)Q[place(r, block) * ld + place(c, block)];
+    qf[r * lq + c] = (float)sym_at(Q, place(r, block), place(c, block), all);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const float finv = (float)inv, step = a.lr * t.scale;
-  for (int64_t i0 = 16 * (threadIdx.x >> 6); i0 < t.len; i0 += 16 * kWaves) {
-    const int64_t i = i0 + c;
-    f32x4 x[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      if (s >= nt) break;
-      float u[4];
-      load_u<4, false>(a, t, i, s * 16 + 4 * g, u);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[s][e] = u[e] * finv;
-    }
-    for (int o = 0; o < nt; ++o) {
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        if (s >= nt) break;
-        acc = Mma<float>::mma(*reinterpret_cast<const f32x4*>(qf + (o * 16 + c) * lq + s * 16 + 4 * g), x[s], acc);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = o * 16 + 4 * g + e;
-        if (i < t.len && j < S) {
-          float* w = t.w + i * t.si + j * t.sj;
-          *w = *w * a.decay - step * acc[e];
-        }
-      }
-    }
+  if constexpr (BIG) {
+    apply<WAVES, 8>(a, t, qf, lq, inv);
+  } else {
+    if (all == 1) apply<WAVES, 1>(a, t, qf, lq, inv);
+    else if (all == 2) apply<WAVES, 2>(a, t, qf, lq, inv);
+    else if (all == 3) apply<WAVES, 3>(a, t, qf, lq, inv);
+    else apply<WAVES, 4>(a, t, qf, lq, inv);
   }
 }
 
@@ -329,7 +423,8 @@ ttc_status check_mats(int64_t n, const ttc_ortho_mat* mats) {
   return TTC_OK;
 }
 
-int padded(int64_t side) { return side <= kLdsSide ? (int)(side + 15) / 16 * 16 : kMaxSide; }
+bool is_big(const ttc_ortho_mat& m) { return std::min(m.rows, m.cols) > kLdsSide; }
+constexpr int64_t kBigSize = 3 * (int64_t)mat_size(kMaxSide / 16);  // doubles of the scratch
 
 }  // namespace
 }  // namespace ttc
@@ -344,7 +439,7 @@ extern "C" ttc_status ttc_ortho_workspace(int64_t n, const ttc_ortho_mat* mats, 
   *plan_bytes = (size_t)n * sizeof(Mat);
   int64_t d = 0;
   for (int64_t k = 0; k < n; ++k)
-    if (std::min(mats[k].rows, mats[k].cols) > kLdsSide) d += 3 * mat_size(kMaxSide);
+    if (is_big(mats[k])) d += kBigSize;
   *scratch_bytes = (size_t)d * sizeof(double);
   return TTC_OK;
 }
@@ -371,14 +466,16 @@ extern "C" ttc_status ttc_ortho_plan(int64_t n, const ttc_ortho_mat* mats, void*
     t.scale = (float)sqrt(std::max(1., (double)m.rows / (double)m.cols));
     if (t.side > kLdsSide) {
       t.scratch = d;
-      d += 3 * mat_size(kMaxSide);
+      d += kBigSize;
     }
     out[k] = t;
   }
-  // the longest first, so that the last work-groups to start are short ones
+  // those of k_ortho<.., true> before the others, and of each kind the longest
+  // first, so that the last work-groups to start are short ones
   std::stable_sort(out, out + n, [](const Mat& x, const Mat& y) {
+    const bool bx = x.side > kLdsSide, by = y.side > kLdsSide;
     const auto cost = [](const Mat& t) { return (double)(t.len + 8 * t.side) * t.side * t.side; };
-    return cost(x) > cost(y);
+    return bx != by ? bx : cost(x) > cost(y);
   });
   return TTC_OK;
 }
@@ -390,7 +487,7 @@ extern "C" ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n, cons
   const float f[] = {desc->a, desc->b, desc->c, desc->eps, desc->lr, desc->mu, desc->weight_decay};
   for (float x : f)
     if (!(fabsf(x) < INFINITY)) return TTC_ERR_SHAPE;
-  if (!(desc->eps > 0.f)) return TTC_ERR_SHAPE;
+  if (!(desc->eps >= FLT_MIN)) return TTC_ERR_SHAPE;
   size_t pb, sb;
   const ttc_status st = ttc_ortho_workspace(n, mats, &pb, &sb);
   if (st != TTC_OK) return st;
@@ -398,12 +495,11 @@ extern "C" ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n, cons
   if (!plan || (sb && !scratch)) return TTC_ERR_NULL;
   if (((uintptr_t)plan | (uintptr_t)scratch) & 15) return TTC_ERR_ALIGN;
   if (plan_bytes < pb || scratch_bytes < sb) return TTC_ERR_WORKSPACE;
-  int64_t side = 1;
-  for (int64_t k = 0; k < n; ++k) side = std::max(side, std::min(mats[k].rows, mats[k].cols));
-  // the three matrices, or the sums of half the waves on their way to the others
-  const int sp = padded(std::min<int64_t>(side, kLdsSide)), nt = sp / 16;
-  const int tiles = side > kLdsSide ? 16 : nt * (nt + 1) / 2;
-  const size_t lds = sizeof(double) * std::max(3 * mat_size(sp), kWaves / 2 * tiles * 256);
+  int64_t big = 0, side = 1;  // the largest side of those that are not big
+  for (int64_t k = 0; k < n; ++k) {
+    if (is_big(mats[k])) ++big;
+    else side = std::max(side, std::min(mats[k].rows, mats[k].cols));
+  }
   OrthoArgs a = {};
   a.mats = static_cast<const Mat*>(plan);
   a.scratch = static_cast<double*>(scratch);
@@ -418,9 +514,21 @@ extern "C" ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n, cons
   a.ahead = desc->nesterov != 0;
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
-  if (lds > 65536)
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_ortho), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  TraceScope ts("ortho", s);
-  TTC_LAUNCH(k_ortho, dim3((unsigned)n), dim3(kThreads), lds, s, a);
+  // dynamic LDS: the three matrices, or the sums of half the waves on their way to the others
+  const auto launch = [&](auto kern, int waves, int64_t count, int tiles, int mats_bytes) {
+    const size_t lds = std::max<size_t>(mats_bytes, sizeof(double) * waves / 2 * std::min(tiles, kSumTiles) * 256);
+    if (lds > 65536)
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    TraceScope ts("ortho", s);
+    TTC_LAUNCH(kern, dim3((unsigned)count), dim3(64 * waves), lds, s, a);
+  };
+  if (big > 0) launch(k_ortho<8, true>, 8, big, 16, 0);
+  if (n > big) {
+    a.mats += big;
+    const int nt = (int)(side + 15) / 16, bytes = 3 * mat_size(nt) * (int)sizeof(double);
+    // up to a matrix a CU, the waves of a CU all take the same one
+    if (n - big <= 256) launch(k_ortho<16, false>, 16, n - big, tiles_of(nt), bytes);
+    else launch(k_ortho<8, false>, 8, n - big, tiles_of(nt), bytes);
+  }
   return hipGetLastError() == hipSuccess ? TTC_OK : TTC_ERR_HIP;
 }
