@@ -32,6 +32,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+class _Sizes:
+    """The bytes of the last call's workspaces: the calls of a program mostly
+    repeat their sizes."""
+
+    def __init__(self):
+        self.key = self.bytes = None
+
+    def get(self, key, query):
+        if key != self.key:
+            self.bytes, self.key = query(), key
+        return self.bytes
+
+
 def _bytes(n: int, device) -> torch.Tensor:
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
@@ -51,9 +64,11 @@ class LayerNorm:
         if self.x_dtype not in (torch.float32, torch.bfloat16) or self.y_dtype not in _ACT:
             raise ValueError(f"no layer norm from {self.x_dtype} to {self.y_dtype}")
         self.desc = make_norm_desc(self.dim, _ACT[self.x_dtype], _ACT[self.y_dtype], eps)
+        self._sizes = _Sizes()
 
     def workspace(self, T: int):
-        return ttc_norm_workspace(self.desc, T)
+        """Bytes of (saved, scratch) for T rows."""
+        return self._sizes.get(T, lambda: ttc_norm_workspace(self.desc, T))
 
     def forward(self, x, gamma, beta, res=None, h=None, out=None, saved=None):
         """(y, h, saved): h = x + res, or x itself without res."""
@@ -125,6 +140,7 @@ class WindowAttention:
         self.kv_heads = self.heads if kv_heads is None else int(kv_heads)
         self.dtype = dtype
         self.desc = make_attn_desc(self.heads, self.dim, self.kv_heads, window[0], window[1], sinks, _ACT[dtype], scale)
+        self._sizes, self._decode_sizes = _Sizes(), _Sizes()
 
     def _seqs(self, q, k, batch, q_offsets, k_offsets, max_q, max_k):
         """Sequences of one length each (``batch`` of them, no offsets) or packed
@@ -147,7 +163,11 @@ class WindowAttention:
 
     def workspace(self, q, k, batch=1, q_offsets=None, k_offsets=None, max_q=None, max_k=None):
         """Bytes of (saved, scratch) of a call with these arguments."""
-        return ttc_attn_workspace(self.desc, self._seqs(q, k, batch, q_offsets, k_offsets, max_q, max_k))
+        return self._workspace(self._seqs(q, k, batch, q_offsets, k_offsets, max_q, max_k))
+
+    def _workspace(self, s):
+        key = s.batch, s.tq, s.tk, s.max_q, s.max_k, bool(s.q_offsets)
+        return self._sizes.get(key, lambda: ttc_attn_workspace(self.desc, s))
 
     def forward(self, q, k, v, batch=1, q_offsets=None, k_offsets=None, max_q=None, out=None, saved=None):
         """(o, saved).  ``max_q``, the longest sequence's queries, sizes the launch
@@ -158,7 +178,7 @@ class WindowAttention:
             out = torch.empty_like(q)
         _need(out, "out", self.dtype, tuple(q.shape))
         if saved is None:
-            saved = _bytes(ttc_attn_workspace(self.desc, seqs)[0], q.device)
+            saved = _bytes(self._workspace(seqs)[0], q.device)
         _need_buf(saved, "saved")
         ttc_attn_fwd(self.desc, seqs, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), saved.data_ptr(),
                      _nbytes(saved), _stream())
@@ -179,7 +199,7 @@ class WindowAttention:
         _need(dk, "dk", self.dtype, tuple(k.shape))
         _need(dv, "dv", self.dtype, tuple(k.shape))
         if scratch is None:
-            scratch = _bytes(ttc_attn_workspace(self.desc, seqs)[1], q.device)
+            scratch = _bytes(self._workspace(seqs)[1], q.device)
         _need_buf(scratch, "scratch")
         ttc_attn_bwd(self.desc, seqs, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
                      saved.data_ptr(), _nbytes(saved), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), scratch.data_ptr(),
@@ -199,7 +219,9 @@ class WindowAttention:
             out = torch.empty_like(q)
         _need(out, "out", self.dtype, tuple(q.shape))
         if scratch is None:
-            scratch = _bytes(ttc_attn_decode_workspace(self.desc, batch, capacity), q.device)
+            need = self._decode_sizes.get((batch, capacity),
+                                          lambda: ttc_attn_decode_workspace(self.desc, batch, capacity))
+            scratch = _bytes(need, q.device)
         _need_buf(scratch, "scratch")
         ttc_attn_decode(self.desc, batch, capacity, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(),
                         out.data_ptr(), scratch.data_ptr(), _nbytes(scratch), _stream())
