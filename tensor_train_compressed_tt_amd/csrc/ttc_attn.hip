@@ -288,6 +288,11 @@ struct Pieces {
   }
 };
 
+// Waits for the wave's loads.  Before a loop that brings tiles, so that the own
+// rows are there on every path into it: else the compiler waits for them inside
+// the loop, and with them for the tile that was just asked for.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
 // the wave's own 32 rows as the right operand (row: this lane's, or none)
 template <typename T, int NS>
 struct Own {
@@ -536,6 +541,7 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_fwd(At
       pk.store(tiles);
       pv.store(tiles + TS);
     }
+    loads_done();
     while (x < kt.hi) {
       const int nx = kt.after(x), j0 = x * kTile;
       lds_barrier();
@@ -656,6 +662,7 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(Att
       pk.store(tiles);
       pv.store(tiles + TS);
     }
+    loads_done();
     while (x < kt.hi) {
       const int nx = kt.after(x), j0 = x * kTile;
       lds_barrier();
@@ -775,6 +782,7 @@ __global__ __launch_bounds__(kThreads, (dkv_groups<T, NS>())) void k_attn_dkv(At
       bring(0, x0);
       put(0);
     }
+    loads_done();
     while (h < group) {
       int nx = x + 1, nh = h;
       if (far && (nx - xf) % kPiece == 0) nx += kPiece * (a.far - 1);
