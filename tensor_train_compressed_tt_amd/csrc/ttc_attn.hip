@@ -982,7 +982,15 @@ __global__ __launch_bounds__(1024) void k_attn_decode(DecodeArgs d) {
   const AttnArgs& a = d.a;
   const int lane = threadIdx.x & 63, r = lane / LPR, x = lane % LPR;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int split = blockIdx.x % d.splits, rest = blockIdx.x / d.splits;
+  // the work-groups of a key head follow each other on one die (see place_of),
+  // whose cache then holds their rows; splits of one long cache are dealt out to
+  // all dies (64 splits of 65536 keys: 39 us, 60 on one die each)
+  int block = blockIdx.x;
+  if (d.chunks > 1 && d.splits == 1) {
+    const int x = blockIdx.x & 7, more = gridDim.x & 7;
+    block = x * (gridDim.x >> 3) + min(x, more) + (blockIdx.x >> 3);
+  }
+  const int split = block % d.splits, rest = block / d.splits;
   const int chunk = rest % d.chunks, hk = rest / d.chunks % a.kv_heads, b = rest / d.chunks / a.kv_heads;
   const int group = a.heads / a.kv_heads, h0 = hk * group + chunk * HG, hn = min(HG, group - chunk * HG);
   const int n = (int)min(max((int64_t)d.lens[b], (int64_t)0), d.capacity);
@@ -1304,7 +1312,10 @@ struct DecodeCut {
 DecodeCut decode_cut(const ttc_attn_desc* d, int64_t batch, int64_t capacity) {
   const int group = d->heads / d->kv_heads;
   DecodeCut c;
-  c.heads = group >= 3 ? 4 : group;
+  // Two of the query heads that share rows at once: half the loads, and half
+  // the registers that four take (16 x 1000, 32 heads of 8: 18 us, with four 24).
+  // One where that leaves CUs without work (1 x 1000, 12 heads of 4: 8 us, with four 15).
+  c.heads = batch * d->kv_heads < 64 ? 1 : std::min(group, 2);
   c.chunks = (group + c.heads - 1) / c.heads;
   const int64_t base = batch * d->kv_heads * c.chunks;
   int64_t most = capacity;  // keys that a query can see
@@ -1323,8 +1334,7 @@ void with_decode(int lanes, int heads, F f) {
   using std::integral_constant;
   const auto by_heads = [&](auto l) {
     if (heads == 1) f(l, integral_constant<int, 1>{});
-    else if (heads == 2) f(l, integral_constant<int, 2>{});
-    else f(l, integral_constant<int, 4>{});
+    else f(l, integral_constant<int, 2>{});
   };
   if (lanes <= 4) by_heads(integral_constant<int, 4>{});
   else if (lanes <= 8) by_heads(integral_constant<int, 8>{});
