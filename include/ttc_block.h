@@ -95,8 +95,9 @@ typedef struct {
  * give where a packed sequence's rows begin; both NULL: every sequence has
  * tq / batch queries and tk / batch keys.  Offsets are cut to [0, tq] and
  * [0, tk] and to ascending order, so wrong ones touch no other memory; rows of
- * no sequence are not written.  max_q and max_k say how many work-groups are
- * worth launching with offsets; results do not depend on them. */
+ * no sequence are not written.  max_q and max_k choose the kernels and the
+ * work-groups of a call with offsets; wrong ones cost time, and results depend
+ * on them by no more than the order of sums. */
 typedef struct {
   int32_t batch;
   int32_t reserved;         /* 0                                            */

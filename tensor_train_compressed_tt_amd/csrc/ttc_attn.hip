@@ -337,23 +337,26 @@ __device__ __forceinline__ f32x16 rows_times_own(const typename Elem<T>::type* t
 // and 8..11 (lanes 0..31) or 4..7 and 12..15 of a 16-row step, by the
 // transposing LDS read (lane 4 j + q of a block of 16 reads row j at columns
 // 4 q .. 4 q + 3, lane i gets column i).
-template <typename T, int NS>
-__device__ __forceinline__ typename Mma<T>::frag col_frag(const typename Elem<T>::type* tile, int half, int s, int dt) {
-  typedef Geo<T, NS> G;
+template <typename T, int LD>
+__device__ __forceinline__ typename Mma<T>::frag col_frag_ld(const typename Elem<T>::type* tile, int half, int s, int dt) {
+  typedef typename Elem<T>::type E;
   const int l = threadIdx.x & 63;
-  if constexpr (sizeof(typename G::E) == 2) {
+  if constexpr (sizeof(E) == 2) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     const int i = l & 15, blk = l >> 4;
-    const typename G::E* p =
-        tile + (32 * half + 16 * s + 4 * (blk >> 1) + (i >> 2)) * G::LD + 32 * dt + 16 * (blk & 1) + 4 * (i & 3);
+    const E* p = tile + (32 * half + 16 * s + 4 * (blk >> 1) + (i >> 2)) * LD + 32 * dt + 16 * (blk & 1) + 4 * (i & 3);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * G::LD));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * LD));
     return __builtin_bit_cast(u16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    const typename G::E* p = tile + (32 * half + 8 * s + 4 * (l >> 5)) * G::LD + 32 * dt + (l & 31);
-    return f32x4{p[0], p[G::LD], p[2 * G::LD], p[3 * G::LD]};
+    const E* p = tile + (32 * half + 8 * s + 4 * (l >> 5)) * LD + 32 * dt + (l & 31);
+    return f32x4{p[0], p[LD], p[2 * LD], p[3 * LD]};
   }
+}
+template <typename T, int NS>
+__device__ __forceinline__ typename Mma<T>::frag col_frag(const typename Elem<T>::type* tile, int half, int s, int dt) {
+  return col_frag_ld<T, Geo<T, NS>::LD>(tile, half, s, dt);
 }
 
 // right operand of k-step s from a result; bf16: rounded to nearest even, half a
@@ -884,6 +887,234 @@ __global__ __launch_bounds__(kThreads) void k_attn_sinks(AttnArgs a) {
   }
 }
 
+// ---- backward of short sequences -----------------------------------------------
+//
+// A work-group takes all of a sequence's keys (at most kShort) for one key head
+// and passes its queries once: the scores are made once for dq, dk and dv, five
+// products instead of the seven of k_attn_dq and k_attn_dkv, and q, k, v and dO
+// are read once instead of twice.  dS goes through LDS, transposed, to the waves
+// that each sum a 32 x 32 piece of dq over all keys.  128 x 128, 12 heads of 64,
+// bf16: 62 us for 200 MB (3.2 TB/s), the two kernels 75 us for 300 MB; two
+// work-groups a CU by their LDS, whose loads and products overlap in part.
+constexpr int kShort = kBlock;
+
+template <typename T, int NS>
+struct ShortGeo {
+  typedef Geo<T, NS> G;
+  static constexpr int LQ = kTile + G::EPV;  // a row of dS: a key's 64 queries
+  static constexpr size_t kLds =
+      (size_t)(4 * kTile * G::LD + kShort * G::LD + kShort * LQ) * sizeof(typename G::E) + kTile * G::CPR * sizeof(float);
+  static constexpr bool kFits = kLds <= 160 * 1024 - 2048;
+  static constexpr int kGroups = 2 * (kLds + 2048) <= 160 * 1024 ? 2 : 1;
+};
+
+// the same, a row at a time, for a sequence that is longer than it was said to be
+template <typename T>
+__device__ __noinline__ void rows_bwd(Mask a, int heads, int kv_heads, int64_t tq, const typename Elem<T>::type* q, const typename Elem<T>::type* o,
+                                      const typename Elem<T>::type* d_o, const typename Elem<T>::type* k,
+                                      const typename Elem<T>::type* v, const float* lse, float* delta,
+                                      typename Elem<T>::type* dq, typename Elem<T>::type* dk,
+                                      typename Elem<T>::type* dv, int lq, int lk) {
+  const int64_t ldq = (int64_t)heads * a.dim, ldk = (int64_t)kv_heads * a.dim;
+  const int group = heads / kv_heads, shift = lk - lq, wave = threadIdx.x >> 6;
+  for (int h = 0; h < group; ++h)
+    for (int i = threadIdx.x; i < lq; i += kThreads)
+      delta[h * tq + i] = dot_row<T>(o + i * ldq + h * a.dim, d_o + i * ldq + h * a.dim, a.dim);
+  __syncthreads();
+  float r[2], r2[2];
+  for (int h = 0; h < group; ++h)
+    for (int i = wave; i < lq; i += kThreads / 64) {
+      const int64_t at = i * ldq + h * a.dim;
+      row_dq<T>(a, q + at, d_o + at, k, v, ldk, i + shift, lk, lse[h * tq + i], delta[h * tq + i], r);
+      row_store<T>(dq + at, r, a.dim);
+    }
+  for (int y = wave; y < lk; y += kThreads / 64) {
+    r[0] = r[1] = r2[0] = r2[1] = 0.f;
+    const int y0 = max(0, y - a.right - shift), y1 = y < a.sinks ? lq : min(lq, y + a.left - shift + 1);
+    for (int h = 0; h < group; ++h)
+      row_dkv<T>(a, q + h * a.dim, d_o + h * a.dim, lse + h * tq, delta + h * tq, ldq, k + y * ldk, v + y * ldk,
+                 y0, y1, r, r2);
+    row_store<T>(dk + y * ldk, r, a.dim);
+    row_store<T>(dv + y * ldk, r2, a.dim);
+  }
+}
+
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_bwd_short(AttnArgs a) {
+  typedef Geo<T, NS> G;
+  typedef typename G::E E;
+  constexpr int TS = kTile * G::LD, LQ = ShortGeo<T, NS>::LQ;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  __shared__ __attribute__((aligned(16))) float stats[2][2][kTile];
+  E* const tiles = reinterpret_cast<E*>(lds_raw);   // two buffers of q and dO
+  E* const keys = tiles + 4 * TS;                   // all of k
+  E* const ds_t = keys + kShort * G::LD;            // dS of a tile, a row a key
+  float* const dots = reinterpret_cast<float*>(ds_t + kShort * LQ);  // dO . o of 16 bytes each
+  const Place w = place_of(a, a.kv_heads);
+  const Span sq = span_of(a.q_off, w.b, a.len_q, a.tq), sk = span_of(a.k_off, w.b, a.len_k, a.tk);
+  const int64_t ldq = (int64_t)a.heads * a.dim, ldk = (int64_t)a.kv_heads * a.dim;
+  const int lbq = (int)ldq * (int)sizeof(E), lbk = (int)ldk * (int)sizeof(E);
+  const int group = a.heads / a.kv_heads, lq = sq.len, lk = sk.len, shift = sk.len - sq.len;
+  const int64_t head = sk.start * ldk + (int64_t)w.head * a.dim;
+  const E *k = static_cast<const E*>(a.k) + head, *v = static_cast<const E*>(a.v) + head;
+  E *dk = static_cast<E*>(a.dk) + head, *dv = static_cast<E*>(a.dv) + head;
+  const int64_t qhead = sq.start * ldq + (int64_t)w.head * group * a.dim;
+  const E *q = static_cast<const E*>(a.q) + qhead, *d_o = static_cast<const E*>(a.d_o) + qhead;
+  const E* o = static_cast<const E*>(a.o_in) + qhead;
+  E* dq = static_cast<E*>(a.dq) + qhead;
+  const float* lse = a.lse + (int64_t)w.head * group * a.tq + sq.start;
+  float* delta = a.delta + (int64_t)w.head * group * a.tq + sq.start;
+  if (lq > kShort || lk > kShort) {
+    rows_bwd<T>(mask_of(a), a.heads, a.kv_heads, a.tq, q, o, d_o, k, v, lse, delta, dq, dk, dv, lq, lk);
+    return;
+  }
+  const int c = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float scale2 = fabsf(a.scale2);
+  const int k0 = kOwn * wave, rows = min(lk - k0, kOwn), j = k0 + c, blocks = (lk + kOwn - 1) / kOwn;
+  const int x1 = (lq + kTile - 1) / kTile;
+  Pieces<T, NS> pq, pd, po;
+  float stat = 0.f;
+  const auto bring = [&](int h, int x) {
+    const int64_t at = (int64_t)x * kTile * ldq + (int64_t)h * a.dim;
+    pq.load(q + at, lq - x * kTile, lbq, a.dim);
+    pd.load(d_o + at, lq - x * kTile, lbq, a.dim);
+    po.load(o + at, lq - x * kTile, lbq, a.dim);
+    if (threadIdx.x < kTile) {
+      const int i = x * kTile + threadIdx.x;
+      stat = i < lq ? lse[(int64_t)h * a.tq + i] : INFINITY;
+    }
+  };
+  const auto put = [&](int b) {
+    pq.store(tiles + b * 2 * TS);
+    pd.store(tiles + b * 2 * TS + TS);
+#pragma unroll
+    for (int n = 0; n < G::NL; ++n) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < G::EPV; ++e) s += elem_to_f32<T>(pd.f[n][e]) * elem_to_f32<T>(po.f[n][e]);
+      dots[threadIdx.x + n * kThreads] = s;
+    }
+    if (threadIdx.x < kTile) stats[b][0][threadIdx.x] = stat;
+  };
+  int h = x1 > 0 ? 0 : group, x = 0, cur = 0;
+  Own<T, NS> kf, vf;
+  if (h < group) {
+    bring(0, 0);
+    Pieces<T, NS> pk[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) pk[y].load(k + (int64_t)y * kTile * ldk, lk - y * kTile, lbk, a.dim);
+    put(0);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) pk[y].store(keys + y * TS);
+  }
+  kf.load(k + (int64_t)k0 * ldk, rows, lbk, a.dim);
+  vf.load(v + (int64_t)k0 * ldk, rows, lbk, a.dim);
+  if (a.scale2 < 0.f) kf.negate();
+  f32x16 ak[NS], av[NS];
+#pragma unroll
+  for (int dt = 0; dt < NS; ++dt) ak[dt] = av[dt] = zero16();
+  loads_done();
+  while (h < group) {
+    const int nx = x + 1 < x1 ? x + 1 : 0, nh = x + 1 < x1 ? h : h + 1;
+    lds_barrier();
+    if (nh < group) bring(nh, nx);
+    if (threadIdx.x < kTile) {
+      float s = 0.f;
+#pragma unroll
+      for (int y = 0; y < G::CPR; ++y) s += dots[threadIdx.x * G::CPR + y];
+      stats[cur][1][threadIdx.x] = s;
+      const int i = x * kTile + threadIdx.x;
+      if (i < lq) delta[(int64_t)h * a.tq + i] = s;
+    }
+    lds_barrier();
+    const E *tq = tiles + cur * 2 * TS, *td = tq + TS;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int i = x * kTile + 32 * hf, p0 = i + shift, p1 = min(i + 31, lq - 1) + shift;
+      if (rows <= 0 || i >= lq || none_seen(a, k0, rows, p0, p1, lk)) continue;
+      f32x16 s = rows_times_own<T, NS>(tq, hf, kf);
+      f32x16 dp = rows_times_own<T, NS>(td, hf, vf);
+      const float *ls = &stats[cur][0][32 * hf + 4 * g], *ds = &stats[cur][1][32 * hf + 4 * g];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + 8 * y), d4 = *reinterpret_cast<const f32x4*>(ds + 8 * y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int z = 4 * y + e;
+          s[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], scale2, -l4[e]));
+          dp[z] = s[z] * (dp[z] - d4[e]);
+        }
+      }
+      if (i + 32 > lq || !all_seen(a, k0, kOwn, p0, p1, lk)) {  // see k_attn_dkv; no query sees a key past the end
+        const int y1 = j >= lk ? 0 : j < a.sinks ? lq : min(lq, j + a.left - shift + 1);
+        const View see(i, max(0, j - a.right - shift), y1, 0);
+        see.cut(s, 0.f);
+        see.cut(dp, 0.f);
+      }
+      cols_times_result<T, NS>(td, hf, s, av);
+      cols_times_result<T, NS>(tq, hf, dp, ak);
+      E* to = ds_t + j * LQ + 32 * hf + 4 * g;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if constexpr (sizeof(E) == 2)
+          *reinterpret_cast<uint2*>(to + 8 * y) = make_uint2(f32x2_to_bf16x2(dp[4 * y], dp[4 * y + 1]),
+                                                             f32x2_to_bf16x2(dp[4 * y + 2], dp[4 * y + 3]));
+        else
+          *reinterpret_cast<f32x4*>(to + 8 * y) = f32x4{dp[4 * y], dp[4 * y + 1], dp[4 * y + 2], dp[4 * y + 3]};
+      }
+    }
+    lds_barrier();
+    for (int u = wave; u < 2 * NS; u += kThreads / 64) {  // 32 queries, 32 of the head's elements
+      const int half = u & 1, dt = u >> 1, i = x * kTile + 32 * half, p0 = i + shift, p1 = min(i + 31, lq - 1) + shift;
+      if (i >= lq) continue;
+      f32x16 acc[1] = {zero16()};
+      for (int b = 0; b < blocks; ++b) {
+        if (none_seen(a, kOwn * b, min(lk - kOwn * b, kOwn), p0, p1, lk)) continue;
+#pragma unroll
+        for (int y = 0; y < G::KP; ++y)
+          acc[0] = Mma32<T>::mma(col_frag<T, NS>(keys, b, y, dt), col_frag_ld<T, LQ>(ds_t, b, y, half), acc[0]);
+      }
+      const int n = min(lq - i, 32);
+      const uint32_t bad = nan_rows(acc) & (n < 32 ? (1u << n) - 1 : ~0u);
+      E* const to = dq + (int64_t)i * ldq + (int64_t)h * a.dim;
+      store_own<T, 1>(to + c * ldq + 32 * dt, c < n && !((bad >> c) & 1), acc, a.scale, a.dim - 32 * dt);
+      for (uint32_t left = bad; left; left &= left - 1) {
+        const int z = __builtin_ctz(left);
+        const int64_t at = (int64_t)(i + z) * ldq + (int64_t)h * a.dim;
+        float r[2];
+        row_dq<T>(mask_of(a), q + at, d_o + at, k, v, ldk, i + z + shift, lk, stats[cur][0][32 * half + z],
+                  stats[cur][1][32 * half + z], r);
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (lane + 64 * y < a.dim && (lane + 64 * y) / 32 == dt) to[z * ldq + lane + 64 * y] = Mma<T>::from_f32(r[y]);
+      }
+    }
+    if (nh < group) {
+      cur ^= 1;
+      put(cur);
+    }
+    x = nx;
+    h = nh;
+  }
+  const uint32_t bad = rows > 0 ? (nan_rows(ak) | nan_rows(av)) & (rows < 32 ? (1u << rows) - 1 : ~0u) : 0;
+  const bool on = c < rows && !((bad >> c) & 1);
+  store_own<T, NS>(dk + (int64_t)j * ldk, on, ak, a.scale, a.dim);
+  store_own<T, NS>(dv + (int64_t)j * ldk, on, av, 1.f, a.dim);
+  __syncthreads();  // delta is there
+  for (uint32_t left = bad; left; left &= left - 1) {
+    const int y = k0 + __builtin_ctz(left);
+    float rk[2] = {0.f, 0.f}, rv[2] = {0.f, 0.f};
+    const int y0 = max(0, y - a.right - shift), y1 = y < a.sinks ? lq : min(lq, y + a.left - shift + 1);
+    for (int hh = 0; hh < group; ++hh)
+      row_dkv<T>(mask_of(a), q + hh * a.dim, d_o + hh * a.dim, lse + (int64_t)hh * a.tq, delta + (int64_t)hh * a.tq, ldq,
+                 k + (int64_t)y * ldk, v + (int64_t)y * ldk, y0, y1, rk, rv);
+    row_store<T>(dk + (int64_t)y * ldk, rk, a.dim);
+    row_store<T>(dv + (int64_t)y * ldk, rv, a.dim);
+  }
+}
+
 // f(T{}, integral constant NS) for the descriptor's type and head size
 template <typename F>
 void with_geo(const ttc_attn_desc* d, F f) {
@@ -911,6 +1142,15 @@ int far_of(const ttc_attn_desc* d, const ttc_attn_seqs* s) {
 size_t far_bytes(const ttc_attn_desc* d, const ttc_attn_seqs* s) {
   const int far = far_of(d, s);
   return far == 0 ? 0 : (size_t)s->batch * d->kv_heads * (1 + far) * 2 * d->sinks * d->dim * sizeof(float);
+}
+
+// Sequences that k_attn_bwd_short takes.  With offsets, the caller's word for the
+// longest; a sequence that is longer all the same is taken row by row.
+bool is_short(const ttc_attn_desc* d, const ttc_attn_seqs* s) {
+  const int64_t q = s->q_offsets ? s->max_q : s->tq / s->batch, k = s->q_offsets ? s->max_k : s->tk / s->batch;
+  bool fits = false;
+  with_geo(d, [&](auto t, auto ns) { fits = ShortGeo<decltype(t), decltype(ns)::value>::kFits; });
+  return fits && s->tq > 0 && s->tk > 0 && q >= 1 && q <= kShort && k >= 1 && k <= kShort;
 }
 
 // two buffers of two tiles
@@ -1265,6 +1505,17 @@ extern "C" ttc_status ttc_attn_bwd(const ttc_attn_desc* desc, const ttc_attn_seq
   a.dv = dv;
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
+  if (is_short(desc, seqs)) {
+    a.tiles = 1;
+    TraceScope ts("attn_bwd", s);
+    with_geo(desc, [&](auto ty, auto ns) {
+      typedef decltype(ty) T;
+      constexpr int NS = decltype(ns)::value;
+      if constexpr (ShortGeo<T, NS>::kFits)
+        launch(k_attn_bwd_short<T, NS>, (unsigned)(a.batch * a.kv_heads), ShortGeo<T, NS>::kLds, s, a);
+    });
+    return launched();
+  }
   if (a.tq > 0) {
     const unsigned grid = grid_of(a, seqs->max_q, a.tq, kBlock, a.heads);
     TraceScope ts("attn_dq", s);

@@ -61,6 +61,7 @@ struct OrthoArgs {
 // further than they are long: in other banks.
 constexpr int kTileLd = 18;
 constexpr int kTileSize = 16 * kTileLd;
+constexpr int kSpareTiles = 3;  // tiles a side up to which two more matrices fit the same room
 constexpr int tiles_of(int nt) { return nt * (nt + 1) / 2; }
 constexpr int mat_size(int nt) { return tiles_of(nt) * kTileSize; }
 __device__ __forceinline__ int tile_at(int p, int q, int nt) { return (p * nt - p * (p - 1) / 2 + q - p) * kTileSize; }
@@ -242,11 +243,22 @@ __device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, 
   return acc;
 }
 
-// A_0 in `A` -> Q in `Q`, over n steps; P is the third matrix.  A wave has at
-// most TPW tiles.
-template <int WAVES, int TPW>
-__device__ void iterate(const OrthoArgs& a, double* A, double* P, double* Q, int nt) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, tiles = tiles_of(nt);
+// A_0 in `A` -> Q, over n steps; returns where Q lies.  P, Q and the spare
+// matrices follow A.  A wave has at most TPW tiles.
+//
+// SPARE: with two more matrices each product goes where nothing is read, so
+// that a stage ends in one barrier; else its results wait in registers for the
+// readers.  A single tile is one wave's work, with no barrier.
+template <int WAVES, int TPW, bool SPARE, bool GLOBAL>
+__device__ double* iterate(const OrthoArgs& a, double* A, int nt) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, tiles = tiles_of(nt), size = mat_size(nt);
+  double *P = A + size, *Q = P + size, *T = SPARE ? Q + size : A, *Q2 = SPARE ? T + size : Q;
+  if (SPARE && tiles == 1 && w > 0) return a.steps & 1 ? Q : Q2;
+  const auto sync = [&] {
+    if constexpr (GLOBAL) __syncthreads();
+    else if (SPARE && tiles == 1) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    else lds_barrier();
+  };
   const int mine = (lane >> 4) * kTileLd + (lane & 15);  // element r of a result: 4 r rows further
   int p[TPW], q[TPW], at[TPW];
 #pragma unroll
@@ -254,105 +266,132 @@ __device__ void iterate(const OrthoArgs& a, double* A, double* P, double* Q, int
     tile_of(min(w + y * WAVES, tiles - 1), nt, p[y], q[y]);
     at[y] = tile_at(p[y], q[y], nt) + mine;
   }
+  const auto each = [&](auto f) {
+#pragma unroll
+    for (int y = 0; y < TPW; ++y) {
+      if (w + y * WAVES >= tiles) break;
+      f(y);
+    }
+  };
+  const auto put = [&](double* to, int y, const f64x4& v) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) to[at[y] + 4 * r * kTileLd] = v[r];
+  };
   for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
+    each([&](int y) {
+      f64x4 s = tile_product(A, A, p[y], q[y], nt);
 #pragma unroll
-    for (int y = 0; y < TPW; ++y) {
-      if (w + y * WAVES >= tiles) break;
-      const f64x4 s = tile_product(A, A, p[y], q[y], nt);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int x = at[y] + 4 * r * kTileLd;
-        const double v = (p[y] == q[y] && 4 * r + (lane >> 4) == (lane & 15) ? a.a : 0.) + a.b * A[x] + a.c * s[r];
-        P[x] = v;
-        if (k == 0) Q[x] = v;
-      }
-    }
-    __syncthreads();
+      for (int r = 0; r < 4; ++r)
+        s[r] = (p[y] == q[y] && 4 * r + (lane >> 4) == (lane & 15) ? a.a : 0.) + a.b * A[at[y] + 4 * r * kTileLd] + a.c * s[r];
+      put(P, y, s);
+      if (k == 0) put(Q, y, s);
+    });
+    sync();
     if (last && k == 0) break;
     f64x4 fa[TPW], fq[TPW];
-#pragma unroll
-    for (int y = 0; y < TPW; ++y) {
-      if (w + y * WAVES >= tiles) break;
+    each([&](int y) {
       if (!last) fa[y] = tile_product(A, P, p[y], q[y], nt);
       if (k > 0) fq[y] = tile_product(Q, P, p[y], q[y], nt);
+    });
+    if (!SPARE) sync();
+    each([&](int y) {
+      if (!last) put(T, y, fa[y]);
+      if (k > 0) put(Q2, y, fq[y]);
+    });
+    sync();
+    if (k > 0) {
+      double* const x = Q;
+      Q = Q2;
+      Q2 = x;
     }
-    __syncthreads();
-#pragma unroll
-    for (int y = 0; y < TPW; ++y) {
-      if (w + y * WAVES >= tiles) break;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int x = at[y] + 4 * r * kTileLd;
-        if (!last) A[x] = fa[y][r];
-        if (k > 0) Q[x] = fq[y][r];
-      }
-    }
-    __syncthreads();
     if (last) break;
+    each([&](int y) { fa[y] = tile_product(T, P, p[y], q[y], nt); });
+    if (!SPARE) sync();
+    each([&](int y) { put(A, y, fa[y]); });
+    sync();
+  }
+  return Q;
+}
+
+// Column (of 16) that entry x of a tile of 16 stands for in Q's fp32 copy.
+// With vectors a lane has four neighbours, entries 4 g .. 4 g + 3; without, the
+// four lanes of a row read neighbours: the lines of 16 rows by 16 bytes instead
+// of 4 (240 x 30: 8.5 -> 3 us).
+template <bool VEC>
+__device__ __forceinline__ int column_of(int x) {
+  return VEC ? x : (x & ~15) + 4 * (x & 3) + ((x >> 2) & 3);
+}
+template <bool VEC>
+__device__ __forceinline__ void load_4(const float* base, const Mat& t, int64_t i, int s, int g, float (&v)[4]) {
+  if constexpr (VEC) {
+    load_n<4, true>(base, t, i, s * 16 + 4 * g, v);
+  } else {
+    i = min(i, t.len - 1);
 #pragma unroll
-    for (int y = 0; y < TPW; ++y) {
-      if (w + y * WAVES >= tiles) break;
-      fa[y] = tile_product(A, P, p[y], q[y], nt);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int y = 0; y < TPW; ++y) {
-      if (w + y * WAVES >= tiles) break;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) A[at[y] + 4 * r * kTileLd] = fa[y][r];
-    }
-    __syncthreads();
+    for (int e = 0; e < 4; ++e) v[e] = base[i * t.si + min(s * 16 + 4 * e + g, t.side - 1) * t.sj];
   }
 }
 
-// w of all rows: 16 rows a wave, NT tiles of 16 columns.  qf: Q in fp32, rows of lq
+// w of all rows: 16 ROWS rows a wave, NT tiles of 16 columns.  qf: Q in fp32, rows of lq
 template <int WAVES, int NT, bool VEC>
 __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv) {
+  constexpr int ROWS = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  constexpr bool AHEAD = NT <= 4;  // w with g and m; of more tiles, one by one
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const float step = a.lr * t.scale;
-  for (int64_t i0 = 16 * (threadIdx.x >> 6); i0 < t.len; i0 += 16 * WAVES) {
-    const int64_t i = i0 + c;
-    constexpr bool AHEAD = NT <= 4;  // w with g and m; of more tiles, one by one
-    float ug[NT][4], um[NT][4], w[AHEAD ? NT : 1][4];
+  for (int64_t i0 = 16 * ROWS * (threadIdx.x >> 6); i0 < t.len; i0 += 16 * ROWS * WAVES) {
+    float ug[ROWS][NT][4], um[ROWS][NT][4], w[ROWS][AHEAD ? NT : 1][4];
 #pragma unroll
-    for (int s = 0; s < NT; ++s) {
-      load_n<4, VEC>(t.g, t, i, s * 16 + 4 * g, ug[s]);
-      load_n<4, VEC>(t.m, t, i, s * 16 + 4 * g, um[s]);
-      if constexpr (AHEAD) load_n<4, VEC>(t.w, t, i, s * 16 + 4 * g, w[s]);
-    }
-    f32x4 x[NT];
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-    for (int s = 0; s < NT; ++s) {
-      float u[4];
-      make_u<4>(a, t, i, s * 16 + 4 * g, ug[s], um[s], u);
+      for (int s = 0; s < NT; ++s) {
+        load_4<VEC>(t.g, t, i0 + 16 * r + c, s, g, ug[r][s]);
+        load_4<VEC>(t.m, t, i0 + 16 * r + c, s, g, um[r][s]);
+        if constexpr (AHEAD) load_4<VEC>(t.w, t, i0 + 16 * r + c, s, g, w[r][s]);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[s][e] = (float)(u[e] * inv);
-    }
-    const auto column = [&](int o, float (&to)[4]) {
-      f32x4 acc = zero4();
+    for (int r = 0; r < ROWS; ++r) {
+      const int64_t i = i0 + 16 * r + c;
+      f32x4 x[NT];
 #pragma unroll
       for (int s = 0; s < NT; ++s)
-        acc = Mma<float>::mma(*reinterpret_cast<const f32x4*>(qf + (o * 16 + c) * lq + s * 16 + 4 * g), x[s], acc);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) to[e] = to[e] * a.decay - step * acc[e];
-      store_n<4, VEC>(t.w, t, i, o * 16 + 4 * g, to);
-    };
-    if constexpr (AHEAD) {
+        for (int e = 0; e < 4; ++e) {
+          const float u = a.ahead ? ug[r][s][e] + a.mu * um[r][s][e] : um[r][s][e];
+          x[s][e] = i < t.len && s * 16 + column_of<VEC>(4 * g + e) < t.side ? (float)(u * inv) : 0.f;
+        }
+      const auto column = [&](int o, float (&to)[4]) {
+        f32x4 acc = zero4();
 #pragma unroll
-      for (int o = 0; o < NT; ++o) column(o, w[o]);
-    } else {
+        for (int s = 0; s < NT; ++s)
+          acc = Mma<float>::mma(*reinterpret_cast<const f32x4*>(qf + (o * 16 + c) * lq + s * 16 + 4 * g), x[s], acc);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = to[e] * a.decay - step * acc[e];
+        if constexpr (VEC) {
+          store_n<4, true>(t.w, t, i, o * 16 + 4 * g, to);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i < t.len && o * 16 + 4 * e + g < t.side) t.w[i * t.si + (o * 16 + 4 * e + g) * t.sj] = to[e];
+        }
+      };
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int o = 0; o < NT; ++o) column(o, w[r][o]);
+      } else {
 #pragma unroll 1
-      for (int o = 0; o < NT; ++o) {
-        load_n<4, VEC>(t.w, t, i, o * 16 + 4 * g, w[0]);
-        column(o, w[0]);
+        for (int o = 0; o < NT; ++o) {
+          load_4<VEC>(t.w, t, i, o, g, w[r][0]);
+          column(o, w[r][0]);
+        }
       }
     }
   }
 }
 template <int WAVES, int NT>
-__device__ __forceinline__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv) {
-  if (vectors(t, 4))
+__device__ __forceinline__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv, bool vec) {
+  if (vec)
     apply<WAVES, NT, true>(a, t, qf, lq, inv);
   else
     apply<WAVES, NT, false>(a, t, qf, lq, inv);
@@ -367,7 +406,7 @@ __global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) 
   const Mat t = a.mats[blockIdx.x];
   const int S = t.side, all = BIG ? kMaxSide / 16 : (S + 15) / 16, block = BIG ? 4 : all;  // tiles of a block of columns
   double* base = BIG ? a.scratch + t.scratch : lds;
-  double *A = base, *P = base + mat_size(all), *Q = P + mat_size(all);
+  double* const A = base;
   if constexpr (BIG) {
     gram<WAVES, 4, true>(a, t, 0, 0, lds, A, all);
     gram<WAVES, 4, true>(a, t, 1, 1, lds, A, all);
@@ -378,33 +417,41 @@ __global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) 
     else if (all == 3) gram<WAVES, 3, true>(a, t, 0, 0, lds, A, all);
     else gram<WAVES, 4, true>(a, t, 0, 0, lds, A, all);
   }
+  // every wave sums the trace, in the same order
   double trace = 0.;
-#pragma unroll 4
-  for (int j = 0; j < 16 * all; ++j) trace += sym_at(A, j, j, all);
+  for (int j = threadIdx.x & 63; j < 16 * all; j += 64) trace += sym_at(A, j, j, all);
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) trace += __shfl_xor(trace, x);
   // a NaN stays one: the comparison with it is false
   const double norm = sqrt(trace), inv = 1. / (norm < (double)a.eps ? (double)a.eps : norm);
   __syncthreads();
 #pragma unroll 4
   for (int x = threadIdx.x; x < mat_size(all); x += 64 * WAVES) A[x] *= inv * inv;
   __syncthreads();
-  iterate<WAVES, (tiles_of(BIG ? kMaxSide / 16 : kLdsSide / 16) + WAVES - 1) / WAVES>(a, A, P, Q, all);
+  const double* Q;
+  if constexpr (BIG) Q = iterate<WAVES, (tiles_of(8) + WAVES - 1) / WAVES, false, true>(a, A, all);
+  else if (all <= kSpareTiles) Q = iterate<WAVES, 1, true, false>(a, A, all);
+  else Q = iterate<WAVES, (tiles_of(4) + WAVES - 1) / WAVES, false, false>(a, A, all);
+  __syncthreads();
 
-  // Q in fp32, in the columns' own order, where A and P were
+  // Q in fp32, in the columns' own order (or column_of), where A and P were
+  const bool vec = vectors(t, 4);
   float* qf = reinterpret_cast<float*>(A);
   const int sp = 16 * all, lq = sp + 4;
 #pragma unroll 4
   for (int x = threadIdx.x; x < sp * sp; x += 64 * WAVES) {
     const int r = x / sp, c = x - r * sp;
-    qf[r * lq + c] = (float)sym_at(Q, place(r, block), place(c, block), all);
+    const int jr = vec ? r : column_of<false>(r), jc = vec ? c : column_of<false>(c);
+    qf[r * lq + c] = (float)sym_at(Q, place(jr, block), place(jc, block), all);
   }
   __syncthreads();
   if constexpr (BIG) {
-    apply<WAVES, 8>(a, t, qf, lq, inv);
+    apply<WAVES, 8>(a, t, qf, lq, inv, vec);
   } else {
-    if (all == 1) apply<WAVES, 1>(a, t, qf, lq, inv);
-    else if (all == 2) apply<WAVES, 2>(a, t, qf, lq, inv);
-    else if (all == 3) apply<WAVES, 3>(a, t, qf, lq, inv);
-    else apply<WAVES, 4>(a, t, qf, lq, inv);
+    if (all == 1) apply<WAVES, 1>(a, t, qf, lq, inv, vec);
+    else if (all == 2) apply<WAVES, 2>(a, t, qf, lq, inv, vec);
+    else if (all == 3) apply<WAVES, 3>(a, t, qf, lq, inv, vec);
+    else apply<WAVES, 4>(a, t, qf, lq, inv, vec);
   }
 }
 
@@ -525,7 +572,7 @@ extern "C" ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n, cons
   if (big > 0) launch(k_ortho<8, true>, 8, big, 16, 0);
   if (n > big) {
     a.mats += big;
-    const int nt = (int)(side + 15) / 16, bytes = 3 * mat_size(nt) * (int)sizeof(double);
+    const int nt = (int)(side + 15) / 16, bytes = (nt <= kSpareTiles ? 5 : 3) * mat_size(nt) * (int)sizeof(double);
     // up to a matrix a CU, the waves of a CU all take the same one
     if (n - big <= 256) launch(k_ortho<16, false>, 16, n - big, tiles_of(nt), bytes);
     else launch(k_ortho<8, false>, 8, n - big, tiles_of(nt), bytes);

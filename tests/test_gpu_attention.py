@@ -464,3 +464,48 @@ def test_sinks_of_long_sequences_see_bad_rows(which, bad):
         _close(cut(x)[~hit], y[~hit], bound[~hit], name)
     if which in ("q", "do"):
         assert not bool(torch.isfinite(got[2][:sinks]).all()), "the sinks are seen by the bad row"
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("d", [8, 32, 56, 64, 80, 128])
+@pytest.mark.parametrize("window,sinks", [((-1, -1), 0), ((-1, 0), 0), ((9, 5), 3), ((40, 0), 70)])
+def test_short_sequences(ty, d, window, sinks):
+    """Packed sequences of at most 128, as the caller says: one work-group has a sequence's backward pass."""
+    lens = [128, 1, 0, 64, 33, 100, 31, 97]
+    _check(lens, lens, h=4, hk=2, d=d, window=window, sinks=sinks, ty=ty, max_q=128, max_k=128, seed=d)
+    _check(lens, [5, 0, 128, 64, 128, 1, 90, 126], h=3, hk=3, d=d, window=window, sinks=sinks, ty=ty, max_q=128, max_k=128, seed=d + 1)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+@pytest.mark.parametrize("lq,lk", [(128, 128), (1, 128), (128, 1), (65, 127), (127, 65)])
+@pytest.mark.parametrize("h,hk", [(1, 1), (8, 1), (6, 2)])
+def test_short_sequences_of_one_length(ty, lq, lk, h, hk):
+    _check([lq] * 3, [lk] * 3, h=h, hk=hk, window=(20, 6), sinks=2, ty=ty, packed=False, seed=lq + lk)
+    _check([lq] * 2, [lk] * 2, h=h, hk=hk, window=(-1, 0), ty=ty, packed=False, scale=-0.2, seed=lq)
+
+
+@pytest.mark.parametrize("ty", [F32, BF16])
+def test_sequences_longer_than_said(ty):
+    """More than 128 rows where the caller said at most 128, among others that are short."""
+    _check([130, 20, 300, 128, 7], [130, 20, 260, 128, 150], h=4, hk=2, d=40, window=(50, 4), sinks=2, ty=ty, max_q=128, max_k=128)
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+def test_short_sequences_with_bad_rows(which):
+    """128 queries and keys of two sequences, a NaN in one row of the first: the other sequence has its values to the bit."""
+    ttc = _ttc()
+    n, d = 128, 64
+    layer = ttc.WindowAttention(4, d, 2, window=(10, 3), sinks=1, dtype=BF16)
+    t = dict(zip(("q", "k", "v", "do"), _inputs([n, n], [n, n], 4, 2, d, BF16, 9)))
+
+    def step():
+        o, saved = layer.forward(t["q"], t["k"], t["v"], batch=2)
+        return (o,) + layer.backward(t["q"], t["k"], t["v"], o, t["do"], saved, batch=2)
+
+    clean = step()
+    t[which][60] = math.nan
+    got = step()
+    for name, x, y in zip(("o", "dq", "dk", "dv"), got, clean):
+        assert torch.equal(x[n:], y[n:]), name
+        far = torch.cat([torch.arange(1, 33), torch.arange(100, n)])  # rows that neither see row 60 nor meet one that does, the sink aside
+        assert bool(torch.isfinite(x[far]).all()), name
