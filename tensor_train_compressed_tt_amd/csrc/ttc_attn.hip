@@ -257,7 +257,10 @@ struct Geo {
   typedef typename Elem<T>::type E;
   static constexpr int DP = 32 * NS;
   static constexpr int EPV = 16 / (int)sizeof(E);
-  static constexpr int LD = DP + EPV;                 // 16 bytes more: rows start in other banks
+  // Rows start in other banks of LDS: 16 bytes further, so that 16 rows' pieces of
+  // 16 bytes lie apart; of 32 and 128 two-byte elements 48 bytes, so that four
+  // rows' 32 bytes, a transposing read, do too.
+  static constexpr int LD = DP + (sizeof(E) == 2 && (NS == 1 || NS == 4) ? 3 * EPV : EPV);
   static constexpr int KF = DP / Mma32<T>::KSTEP;     // k-steps over the head's elements
   static constexpr int KP = kTile / 2 / Mma32<T>::KSTEP;  // k-steps over 32 rows of a tile
   static constexpr int CPR = DP / EPV;                // 16-byte pieces of a row

@@ -251,7 +251,9 @@ __device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, 
 // readers.  A single tile is one wave's work, with no barrier.
 template <int WAVES, int TPW, bool SPARE, bool GLOBAL>
 __device__ double* iterate(const OrthoArgs& a, double* A, int nt) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, tiles = tiles_of(nt), size = mat_size(nt);
+  const int lane = threadIdx.x & 63, tiles = tiles_of(nt), size = mat_size(nt);
+  // waves of neighbouring work-groups begin at other tiles: two of 10 tiles that share a CU load its SIMDs alike
+  const int w = SPARE ? threadIdx.x >> 6 : ((threadIdx.x >> 6) + 2 * (blockIdx.x >> 8 & 1)) % WAVES;
   double *P = A + size, *Q = P + size, *T = SPARE ? Q + size : A, *Q2 = SPARE ? T + size : Q;
   if (SPARE && tiles == 1 && w > 0) return a.steps & 1 ? Q : Q2;
   const auto sync = [&] {
