@@ -232,13 +232,28 @@ __device__ __forceinline__ void tile_of(int x, int nt, int& p, int& q) {
 __device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, int p, int q, int nt) {
   const int lane = threadIdx.x & 63, along = (lane & 15) * kTileLd + (lane >> 4), across = (lane >> 4) * kTileLd + (lane & 15);
   f64x4 acc = {0., 0., 0., 0.};
-#pragma unroll 1
-  for (int b = 0; b < nt; ++b) {  // rows p and q of the tiles' column b, or of row b turned over
+  double px[4], py[4], nx[4], ny[4];
+  // rows p and q of the tiles' column b, or of row b turned over
+  const auto load = [&](int b, double (&u)[4], double (&v)[4]) {
     const double* rx = x + (b >= p ? tile_at(p, b, nt) + along : tile_at(b, p, nt) + across);
     const double* ry = y + (b >= q ? tile_at(q, b, nt) + along : tile_at(b, q, nt) + across);
     const int sx = b >= p ? 4 : 4 * kTileLd, sy = b >= q ? 4 : 4 * kTileLd;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc = mma64(rx[k * sx], ry[k * sy], acc);
+    for (int k = 0; k < 4; ++k) {
+      u[k] = rx[k * sx];
+      v[k] = ry[k * sy];
+    }
+  };
+  load(0, px, py);
+#pragma unroll 1
+  for (int b = 0; b < nt; ++b) {  // the next tiles come while these are multiplied
+    load(min(b + 1, nt - 1), nx, ny);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc = mma64(px[k], py[k], acc);
+      px[k] = nx[k];
+      py[k] = ny[k];
+    }
   }
   return acc;
 }
