@@ -331,27 +331,40 @@ __device__ double* iterate(const OrthoArgs& a, double* A, int nt) {
   return Q;
 }
 
-// Column (of 16) that entry x of a tile of 16 stands for in Q's fp32 copy.
-// With vectors a lane has four neighbours, entries 4 g .. 4 g + 3; without, the
-// four lanes of a row read neighbours: the lines of 16 rows by 16 bytes instead
-// of 4 (240 x 30: 8.5 -> 3 us).
-template <bool VEC>
+// Column (of 16) that entry x of a tile of 16 stands for in Q's fp32 copy, where
+// W neighbours are read at once.  With four, a lane's entries 4 g .. 4 g + 3 are
+// neighbours; with fewer, the four lanes of a row read W neighbours each, so that
+// a load meets its 16 rows' lines with 16 W bytes of each (480 x 30, by twos: 15 ->
+// 8 us of its work-group's time).
+template <int W>
 __device__ __forceinline__ int column_of(int x) {
-  return VEC ? x : (x & ~15) + 4 * (x & 3) + ((x >> 2) & 3);
+  const int g = (x >> 2) & 3, e = x & 3;
+  return (x & ~15) + (W == 4 ? 4 * g + e : W == 2 ? 8 * (e >> 1) + 2 * g + (e & 1) : 4 * e + g);
 }
-template <bool VEC>
+// the four entries 4 g .. 4 g + 3 of tile s in row i
+template <int W>
 __device__ __forceinline__ void load_4(const float* base, const Mat& t, int64_t i, int s, int g, float (&v)[4]) {
-  if constexpr (VEC) {
-    load_n<4, true>(base, t, i, s * 16 + 4 * g, v);
-  } else {
-    i = min(i, t.len - 1);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = base[i * t.si + min(s * 16 + 4 * e + g, t.side - 1) * t.sj];
+  for (int e = 0; e < 4; e += W) {
+    float x[W];
+    load_n<W, (W > 1)>(base, t, i, s * 16 + column_of<W>(4 * g + e), x);
+#pragma unroll
+    for (int y = 0; y < W; ++y) v[e + y] = x[y];
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_4(float* base, const Mat& t, int64_t i, int s, int g, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += W) {
+    float x[W];
+#pragma unroll
+    for (int y = 0; y < W; ++y) x[y] = v[e + y];
+    store_n<W, (W > 1)>(base, t, i, s * 16 + column_of<W>(4 * g + e), x);
   }
 }
 
 // w of all rows: 16 ROWS rows a wave, NT tiles of 16 columns.  qf: Q in fp32, rows of lq
-template <int WAVES, int NT, bool VEC>
+template <int WAVES, int NT, int W>
 __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv) {
   constexpr int ROWS = NT == 1 ? 4 : NT == 2 ? 2 : 1;
   constexpr bool AHEAD = NT <= 4;  // w with g and m; of more tiles, one by one
@@ -363,9 +376,9 @@ __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq,
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
       for (int s = 0; s < NT; ++s) {
-        load_4<VEC>(t.g, t, i0 + 16 * r + c, s, g, ug[r][s]);
-        load_4<VEC>(t.m, t, i0 + 16 * r + c, s, g, um[r][s]);
-        if constexpr (AHEAD) load_4<VEC>(t.w, t, i0 + 16 * r + c, s, g, w[r][s]);
+        load_4<W>(t.g, t, i0 + 16 * r + c, s, g, ug[r][s]);
+        load_4<W>(t.m, t, i0 + 16 * r + c, s, g, um[r][s]);
+        if constexpr (AHEAD) load_4<W>(t.w, t, i0 + 16 * r + c, s, g, w[r][s]);
       }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -376,7 +389,7 @@ __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float u = a.ahead ? ug[r][s][e] + a.mu * um[r][s][e] : um[r][s][e];
-          x[s][e] = i < t.len && s * 16 + column_of<VEC>(4 * g + e) < t.side ? (float)(u * inv) : 0.f;
+          x[s][e] = i < t.len && s * 16 + column_of<W>(4 * g + e) < t.side ? (float)(u * inv) : 0.f;
         }
       const auto column = [&](int o, float (&to)[4]) {
         f32x4 acc = zero4();
@@ -385,13 +398,7 @@ __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq,
           acc = Mma<float>::mma(*reinterpret_cast<const f32x4*>(qf + (o * 16 + c) * lq + s * 16 + 4 * g), x[s], acc);
 #pragma unroll
         for (int e = 0; e < 4; ++e) to[e] = to[e] * a.decay - step * acc[e];
-        if constexpr (VEC) {
-          store_n<4, true>(t.w, t, i, o * 16 + 4 * g, to);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (i < t.len && o * 16 + 4 * e + g < t.side) t.w[i * t.si + (o * 16 + 4 * e + g) * t.sj] = to[e];
-        }
+        store_4<W>(t.w, t, i, o, g, to);
       };
       if constexpr (AHEAD) {
 #pragma unroll
@@ -399,7 +406,7 @@ __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq,
       } else {
 #pragma unroll 1
         for (int o = 0; o < NT; ++o) {
-          load_4<VEC>(t.w, t, i, o, g, w[r][0]);
+          load_4<W>(t.w, t, i, o, g, w[r][0]);
           column(o, w[r][0]);
         }
       }
@@ -407,11 +414,13 @@ __device__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq,
   }
 }
 template <int WAVES, int NT>
-__device__ __forceinline__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv, bool vec) {
-  if (vec)
-    apply<WAVES, NT, true>(a, t, qf, lq, inv);
+__device__ __forceinline__ void apply(const OrthoArgs& a, const Mat& t, const float* qf, int lq, double inv, int vec) {
+  if (vec == 4)
+    apply<WAVES, NT, 4>(a, t, qf, lq, inv);
+  else if (vec == 2)
+    apply<WAVES, NT, 2>(a, t, qf, lq, inv);
   else
-    apply<WAVES, NT, false>(a, t, qf, lq, inv);
+    apply<WAVES, NT, 1>(a, t, qf, lq, inv);
 }
 
 // BIG: a side over kLdsSide, whose S x S matrices lie in the scratch.  A SIMD
@@ -452,13 +461,14 @@ __global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) 
   __syncthreads();
 
   // Q in fp32, in the columns' own order (or column_of), where A and P were
-  const bool vec = vectors(t, 4);
+  const int vec = vectors(t, 4) ? 4 : vectors(t, 2) ? 2 : 1;
   float* qf = reinterpret_cast<float*>(A);
   const int sp = 16 * all, lq = sp + 4;
 #pragma unroll 4
   for (int x = threadIdx.x; x < sp * sp; x += 64 * WAVES) {
     const int r = x / sp, c = x - r * sp;
-    const int jr = vec ? r : column_of<false>(r), jc = vec ? c : column_of<false>(c);
+    const int jr = vec == 4 ? r : vec == 2 ? column_of<2>(r) : column_of<1>(r);
+    const int jc = vec == 4 ? c : vec == 2 ? column_of<2>(c) : column_of<1>(c);
     qf[r * lq + c] = (float)sym_at(Q, place(jr, block), place(jc, block), all);
   }
   __syncthreads();
