@@ -14,7 +14,9 @@
 //
 // One work-group takes one matrix from start to end: the S x S work needs one
 // CU's LDS and no launch of its own, and the work-groups of a step, which are
-// in different phases, share memory and matrix units.
+// in different phases, share memory and matrix units.  What one CU reads in a
+// second is little of what the card does, so a matrix of very many rows has its
+// two passes over them (A_0 and X_0 Q) cut into chunks of their own work-groups.
 #include <hip/hip_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -34,6 +36,11 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 constexpr int kMaxSide = 128;
 constexpr int kMaxSteps = 32;
 constexpr int kLdsSide = 64;  // the S x S matrices of larger ones lie in the scratch
+// Rows from which on a matrix is long, and the chunks that its rows are cut into.
+// One work-group passes 4096 rows of 16 twice in 35 us; the two launches of
+// chunks take 5 us each, which 2048 rows just repay.
+constexpr int64_t kLong = 2048;
+constexpr int kChunks = 32;
 
 // A matrix as the kernel sees it: element (i, j), i < len along the long side,
 // j < side along the short one, is at i * si + j * sj.
@@ -42,7 +49,7 @@ struct Mat {
   const float* g;
   float* m;
   int64_t len, si, sj;
-  int64_t scratch;  // doubles from the scratch's start on (side > kLdsSide)
+  int64_t scratch;  // of big and long ones: doubles from the scratch's start on
   int32_t side;
   float scale;  // sqrt(max(1, rows / cols))
 };
@@ -61,9 +68,10 @@ struct OrthoArgs {
 // further than they are long: in other banks.
 constexpr int kTileLd = 18;
 constexpr int kTileSize = 16 * kTileLd;
+__host__ __device__ constexpr bool is_long(int64_t len, int64_t side) { return len > kLong && side <= kLdsSide; }
 constexpr int kSpareTiles = 3;  // tiles a side up to which two more matrices fit the same room
-constexpr int tiles_of(int nt) { return nt * (nt + 1) / 2; }
-constexpr int mat_size(int nt) { return tiles_of(nt) * kTileSize; }
+__host__ __device__ constexpr int tiles_of(int nt) { return nt * (nt + 1) / 2; }
+__host__ __device__ constexpr int mat_size(int nt) { return tiles_of(nt) * kTileSize; }
 __device__ __forceinline__ int tile_at(int p, int q, int nt) { return (p * nt - p * (p - 1) / 2 + q - p) * kTileSize; }
 __device__ __forceinline__ double sym_at(const double* x, int row, int col, int nt) {
   const int p = row >> 4, q = col >> 4;
@@ -113,6 +121,9 @@ __device__ __forceinline__ bool vectors(const Mat& t, int n) {
   const uintptr_t all = (uintptr_t)t.w | (uintptr_t)t.g | (uintptr_t)t.m;
   return t.sj == 1 && t.side % n == 0 && all % (4 * n) == 0;
 }
+
+// elements of a row that k_ortho's last pass takes at once
+__device__ __forceinline__ int access_of(const Mat& t) { return vectors(t, 4) ? 4 : vectors(t, 2) ? 2 : 1; }
 
 // U rows of N elements of u from what was loaded; zeros outside the matrix
 template <int N>
@@ -423,6 +434,53 @@ __device__ __forceinline__ void apply(const OrthoArgs& a, const Mat& t, const fl
     apply<WAVES, NT, 1>(a, t, qf, lq, inv);
 }
 
+template <int WAVES>
+__device__ __forceinline__ void gram_of(const OrthoArgs& a, const Mat& t, int nt, double* lds, double* out) {
+  if (nt == 1) gram<WAVES, 1, true>(a, t, 0, 0, lds, out, nt);
+  else if (nt == 2) gram<WAVES, 2, true>(a, t, 0, 0, lds, out, nt);
+  else if (nt == 3) gram<WAVES, 3, true>(a, t, 0, 0, lds, out, nt);
+  else gram<WAVES, 4, true>(a, t, 0, 0, lds, out, nt);
+}
+template <int WAVES>
+__device__ __forceinline__ void apply_of(const OrthoArgs& a, const Mat& t, int nt, const float* qf, double inv) {
+  const int vec = access_of(t), lq = 16 * nt + 4;
+  if (nt == 1) apply<WAVES, 1>(a, t, qf, lq, inv, vec);
+  else if (nt == 2) apply<WAVES, 2>(a, t, qf, lq, inv, vec);
+  else if (nt == 3) apply<WAVES, 3>(a, t, qf, lq, inv, vec);
+  else apply<WAVES, 4>(a, t, qf, lq, inv, vec);
+}
+
+// A long matrix's part of the scratch: A_0 of each chunk, then 1 / |U|, then Q in fp32
+__host__ __device__ constexpr int64_t long_inv(int nt) { return (int64_t)kChunks * mat_size(nt); }
+__host__ __device__ constexpr int64_t long_size(int nt) { return long_inv(nt) + 2 + 16 * nt * (16 * nt + 4) / 2; }
+
+// rows of chunk blockIdx.x % kChunks of matrix blockIdx.x / kChunks
+__device__ __forceinline__ Mat chunk_of(const OrthoArgs& a) {
+  Mat t = a.mats[blockIdx.x / kChunks];
+  const int64_t per = (t.len + kChunks - 1) / kChunks, r0 = min(t.len, blockIdx.x % kChunks * per);
+  t.len = min(t.len - r0, per);
+  t.w += r0 * t.si;
+  t.g += r0 * t.si;
+  t.m += r0 * t.si;
+  return t;
+}
+constexpr int kChunkWaves = 8;
+__global__ __launch_bounds__(64 * kChunkWaves, 4) void k_ortho_gram(OrthoArgs a) {
+  extern __shared__ __attribute__((aligned(16))) double lds[];
+  const Mat t = chunk_of(a);
+  const int nt = (t.side + 15) / 16;
+  gram_of<kChunkWaves>(a, t, nt, lds, a.scratch + t.scratch + (int64_t)(blockIdx.x % kChunks) * mat_size(nt));
+}
+__global__ __launch_bounds__(64 * kChunkWaves, 4) void k_ortho_apply(OrthoArgs a) {
+  __shared__ __attribute__((aligned(16))) float qf[kLdsSide * (kLdsSide + 4)];
+  const Mat t = chunk_of(a);
+  const int nt = (t.side + 15) / 16;
+  const double* from = a.scratch + t.scratch + long_inv(nt);
+  for (int x = threadIdx.x; x < 16 * nt * (16 * nt + 4); x += 64 * kChunkWaves) qf[x] = reinterpret_cast<const float*>(from + 2)[x];
+  __syncthreads();
+  apply_of<kChunkWaves>(a, t, nt, qf, from[0]);
+}
+
 // BIG: a side over kLdsSide, whose S x S matrices lie in the scratch.  A SIMD
 // holds four waves (128 registers each), two where the 16 tiles of a block of
 // a large Gram matrix are summed.
@@ -438,10 +496,18 @@ __global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) 
     gram<WAVES, 4, true>(a, t, 1, 1, lds, A, all);
     gram<WAVES, 4, false>(a, t, 0, 1, lds, A, all);
   } else {
-    if (all == 1) gram<WAVES, 1, true>(a, t, 0, 0, lds, A, all);
-    else if (all == 2) gram<WAVES, 2, true>(a, t, 0, 0, lds, A, all);
-    else if (all == 3) gram<WAVES, 3, true>(a, t, 0, 0, lds, A, all);
-    else gram<WAVES, 4, true>(a, t, 0, 0, lds, A, all);
+    if (is_long(t.len, S)) {  // k_ortho_gram's sums, in order
+      const double* part = a.scratch + t.scratch;
+      for (int x = threadIdx.x; x < mat_size(all); x += 64 * WAVES) {
+        double s = 0.;
+#pragma unroll 8
+        for (int y = 0; y < kChunks; ++y) s += part[y * mat_size(all) + x];
+        A[x] = s;
+      }
+      __syncthreads();
+    } else {
+      gram_of<WAVES>(a, t, all, lds, A);
+    }
   }
   // every wave sums the trace, in the same order
   double trace = 0.;
@@ -461,7 +527,7 @@ __global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) 
   __syncthreads();
 
   // Q in fp32, in the columns' own order (or column_of), where A and P were
-  const int vec = vectors(t, 4) ? 4 : vectors(t, 2) ? 2 : 1;
+  const int vec = access_of(t);
   float* qf = reinterpret_cast<float*>(A);
   const int sp = 16 * all, lq = sp + 4;
 #pragma unroll 4
@@ -475,10 +541,13 @@ __global__ __launch_bounds__(64 * WAVES, BIG ? 2 : 4) void k_ortho(OrthoArgs a) 
   if constexpr (BIG) {
     apply<WAVES, 8>(a, t, qf, lq, inv, vec);
   } else {
-    if (all == 1) apply<WAVES, 1>(a, t, qf, lq, inv, vec);
-    else if (all == 2) apply<WAVES, 2>(a, t, qf, lq, inv, vec);
-    else if (all == 3) apply<WAVES, 3>(a, t, qf, lq, inv, vec);
-    else apply<WAVES, 4>(a, t, qf, lq, inv, vec);
+    if (is_long(t.len, S)) {  // for k_ortho_apply
+      double* to = a.scratch + t.scratch + long_inv(all);
+      if (threadIdx.x == 0) to[0] = inv;
+      for (int x = threadIdx.x; x < sp * lq; x += 64 * WAVES) reinterpret_cast<float*>(to + 2)[x] = qf[x];
+    } else {
+      apply_of<WAVES>(a, t, all, qf, inv);
+    }
   }
 }
 
@@ -498,7 +567,12 @@ ttc_status check_mats(int64_t n, const ttc_ortho_mat* mats) {
 }
 
 bool is_big(const ttc_ortho_mat& m) { return std::min(m.rows, m.cols) > kLdsSide; }
-constexpr int64_t kBigSize = 3 * (int64_t)mat_size(kMaxSide / 16);  // doubles of the scratch
+bool is_long(const ttc_ortho_mat& m) { return is_long(std::max(m.rows, m.cols), std::min(m.rows, m.cols)); }
+// doubles of the scratch that a matrix takes
+int64_t scratch_of(const ttc_ortho_mat& m) {
+  if (is_big(m)) return 3 * (int64_t)mat_size(kMaxSide / 16);
+  return is_long(m) ? long_size((int)(std::min(m.rows, m.cols) + 15) / 16) : 0;
+}
 
 }  // namespace
 }  // namespace ttc
@@ -512,8 +586,7 @@ extern "C" ttc_status ttc_ortho_workspace(int64_t n, const ttc_ortho_mat* mats, 
   if (st != TTC_OK) return st;
   *plan_bytes = (size_t)n * sizeof(Mat);
   int64_t d = 0;
-  for (int64_t k = 0; k < n; ++k)
-    if (is_big(mats[k])) d += kBigSize;
+  for (int64_t k = 0; k < n; ++k) d += scratch_of(mats[k]);
   *scratch_bytes = (size_t)d * sizeof(double);
   return TTC_OK;
 }
@@ -538,18 +611,16 @@ extern "C" ttc_status ttc_ortho_plan(int64_t n, const ttc_ortho_mat* mats, void*
     t.si = tall ? m.cols : 1;
     t.sj = tall ? 1 : m.cols;
     t.scale = (float)sqrt(std::max(1., (double)m.rows / (double)m.cols));
-    if (t.side > kLdsSide) {
-      t.scratch = d;
-      d += kBigSize;
-    }
+    t.scratch = d;
+    d += scratch_of(m);
     out[k] = t;
   }
-  // those of k_ortho<.., true> before the others, and of each kind the longest
-  // first, so that the last work-groups to start are short ones
+  // big ones, long ones, the others, and of each kind the longest first, so that
+  // the last work-groups to start are short ones
   std::stable_sort(out, out + n, [](const Mat& x, const Mat& y) {
-    const bool bx = x.side > kLdsSide, by = y.side > kLdsSide;
+    const auto kind = [](const Mat& t) { return t.side > kLdsSide ? 0 : is_long(t.len, t.side) ? 1 : 2; };
     const auto cost = [](const Mat& t) { return (double)(t.len + 8 * t.side) * t.side * t.side; };
-    return bx != by ? bx : cost(x) > cost(y);
+    return kind(x) != kind(y) ? kind(x) < kind(y) : cost(x) > cost(y);
   });
   return TTC_OK;
 }
@@ -569,10 +640,11 @@ extern "C" ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n, cons
   if (!plan || (sb && !scratch)) return TTC_ERR_NULL;
   if (((uintptr_t)plan | (uintptr_t)scratch) & 15) return TTC_ERR_ALIGN;
   if (plan_bytes < pb || scratch_bytes < sb) return TTC_ERR_WORKSPACE;
-  int64_t big = 0, side = 1;  // the largest side of those that are not big
+  int64_t big = 0, longs = 0, side = 1;  // the largest side of those that are not big
   for (int64_t k = 0; k < n; ++k) {
     if (is_big(mats[k])) ++big;
     else side = std::max(side, std::min(mats[k].rows, mats[k].cols));
+    longs += is_long(mats[k]);
   }
   OrthoArgs a = {};
   a.mats = static_cast<const Mat*>(plan);
@@ -589,20 +661,22 @@ extern "C" ttc_status ttc_ortho_step(const ttc_ortho_desc* desc, int64_t n, cons
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
   // dynamic LDS: the three matrices, or the sums of half the waves on their way to the others
-  const auto launch = [&](auto kern, int waves, int64_t count, int tiles, int mats_bytes) {
+  const auto launch = [&](const char* name, auto kern, int waves, int64_t count, int tiles, int mats_bytes) {
     const size_t lds = std::max<size_t>(mats_bytes, sizeof(double) * waves / 2 * std::min(tiles, kSumTiles) * 256);
     if (lds > 65536)
       (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    TraceScope ts("ortho", s);
+    TraceScope ts(name, s);
     TTC_LAUNCH(kern, dim3((unsigned)count), dim3(64 * waves), lds, s, a);
   };
-  if (big > 0) launch(k_ortho<8, true>, 8, big, 16, 0);
+  if (big > 0) launch("ortho", k_ortho<8, true>, 8, big, 16, 0);
   if (n > big) {
     a.mats += big;
     const int nt = (int)(side + 15) / 16, bytes = (nt <= kSpareTiles ? 5 : 3) * mat_size(nt) * (int)sizeof(double);
+    if (longs > 0) launch("ortho_gram", k_ortho_gram, kChunkWaves, longs * kChunks, tiles_of(nt), 0);
     // up to a matrix a CU, the waves of a CU all take the same one
-    if (n - big <= 256) launch(k_ortho<16, false>, 16, n - big, tiles_of(nt), bytes);
-    else launch(k_ortho<8, false>, 8, n - big, tiles_of(nt), bytes);
+    if (n - big <= 256) launch("ortho", k_ortho<16, false>, 16, n - big, tiles_of(nt), bytes);
+    else launch("ortho", k_ortho<8, false>, 8, n - big, tiles_of(nt), bytes);
+    if (longs > 0) launch("ortho_apply", k_ortho_apply, kChunkWaves, longs * kChunks, 0, 0);
   }
   return hipGetLastError() == hipSuccess ? TTC_OK : TTC_ERR_HIP;
 }

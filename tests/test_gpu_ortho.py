@@ -203,3 +203,39 @@ def test_refusals():
         ttc.OrthogonalUpdate([z(4, 4)], [z(4, 4)], [z(4, 4)], steps=0).step(0.1)
     assert e.value.code == 2
     ttc.OrthogonalUpdate([], [], []).step(0.1)
+
+
+@pytest.mark.parametrize("side", [1, 15, 16, 30, 33, 48, 64])
+@pytest.mark.parametrize("length", [2047, 2048, 2049, 4096, 5003])
+def test_long_matrices(side, length):
+    """Around the length from which on a matrix's rows are cut into chunks, next to short and to big ones."""
+    _check([(length, side), (40, 30), (side, length), (100, 70)], seed=length + side)
+
+
+def test_very_long_matrix():
+    _check([(200001, 20)], seed=3)
+
+
+def test_long_matrices_repeat_and_stay_apart():
+    """Bitwise the same on every call and in a replayed graph; a NaN stays in its matrix."""
+    ttc = _ttc()
+    shapes = [(4096, 16), (5000, 30), (100, 20), (3000, 64)]
+    a, b, c = (_matrices(shapes, 9) for _ in range(3))
+    upd = [ttc.OrthogonalUpdate(*[[t[k] for t in x] for k in range(3)]) for x in (a, b, c)]
+    for u in upd[:2]:
+        for _ in range(4):
+            u.step(0.1)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for s, t in zip(a, b) for p, q in zip(s, t))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        upd[2].step(0.1)
+    for _ in range(4):
+        g.replay()
+        torch.cuda.synchronize()
+        upd[0].step(0.1)  # eager work between the replays
+    assert all(torch.equal(p, q) for s, t in zip(b, c) for p, q in zip(s, t))
+    b[1][1][4000, 7] = math.nan
+    for u in upd[1:]:
+        u.step(0.1)
+    assert bool(torch.isnan(b[1][0]).all()) and all(torch.equal(b[k][0], c[k][0]) for k in (0, 2, 3))
