@@ -311,6 +311,13 @@ struct Own {
       f[k] = buf_frag<T>(r, c < rows && d < dim ? (uint32_t)(c * ldb + d * (int)sizeof(typename G::E)) : kNoOff);
     }
   }
+  // these rows (of the result) times those
+  __device__ __forceinline__ f32x16 times(const Own& own) const {
+    f32x16 c = zero16();
+#pragma unroll
+    for (int k = 0; k < G::KF; ++k) c = Mma32<T>::mma(f[k], own.f[k], c);
+    return c;
+  }
   __device__ __forceinline__ void negate() {
 #pragma unroll
     for (int k = 0; k < G::KF; ++k)
@@ -614,6 +621,22 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_fwd(At
   }
 }
 
+// delta = dO . o carries the rounding of a bf16 o, which is small beside dP - delta
+// where o is a mean of many values, but not where a query sees few: dq and dk of a
+// window of 2 were off by 0.6 % of their norm, of which the rounding of P and dS
+// is 0.2.  A wave with a query that sees less than kFewKeys keys takes delta_i =
+// sum_j P_ij dP_ij instead, by two products more for those keys.
+constexpr int kFewKeys = 32;
+__device__ __forceinline__ int keys_seen(const AttnArgs& a, int p, int lk) {
+  const int hi = min(lk, p + a.right + 1), lo = max(0, p - a.left);
+  return max(0, hi - lo) + max(0, min(min(a.sinks, lo), hi));
+}
+// of the queries at places p0 .. p1; the number falls or rises towards both ends of a sequence alone
+template <typename E>
+__device__ __forceinline__ bool few_keys(const AttnArgs& a, int p0, int p1, int lk) {
+  return sizeof(E) == 2 && min(keys_seen(a, p0, lk), keys_seen(a, p1, lk)) < kFewKeys;
+}
+
 // dq, and delta for k_attn_dkv
 template <typename T, int NS>
 __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(AttnArgs a) {
@@ -651,11 +674,31 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(Att
 #pragma unroll
       for (int e = 0; e < G::EPV; ++e) dl += elem_to_f32<T>(of.f[f][e]) * elem_to_f32<T>(qf.f[f][e]);
     dl = sum_halves(dl);
-    if (c < rows && g == 0) delta[q0 + c] = dl;
     of = qf;  // dO
     qf.load(q + (int64_t)q0 * ldq, rows, lbq, a.dim);
     if (a.scale2 < 0.f) qf.negate();
     const float sub = c < rows ? lse[q0 + c] : INFINITY;
+    if (rows > 0 && few_keys<E>(a, p0, p1, lk)) {
+      float sum = 0.f;
+      for (int x = kt.first(); x < kt.hi; x = kt.after(x)) {
+#pragma unroll 1
+        for (int j = x * kTile; j < (x + 1) * kTile; j += kOwn) {
+          if (none_seen(a, j, kOwn, p0, p1, lk)) continue;
+          Own<T, NS> kr;
+          kr.load(k + (int64_t)j * ldk, lk - j, lbk, a.dim);
+          f32x16 s = kr.times(qf);
+          kr.load(v + (int64_t)j * ldk, lk - j, lbk, a.dim);
+          const f32x16 dp = kr.times(of);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * dp[i];
+          if (!all_seen(a, j, kOwn, p0, p1, lk)) key_view(a, j, p, lk).cut(s, 0.f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum += s[i];
+        }
+      }
+      dl = sum_halves(sum);
+    }
+    if (c < rows && g == 0) delta[q0 + c] = dl;
     f32x16 acc[NS];
 #pragma unroll
     for (int dt = 0; dt < NS; ++dt) acc[dt] = zero16();
@@ -897,7 +940,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_sinks(AttnArgs a) {
 // products instead of the seven of k_attn_dq and k_attn_dkv, and q, k, v and dO
 // are read once instead of twice.  dS goes through LDS, transposed, to the waves
 // that each sum a 32 x 32 piece of dq over all keys.  128 x 128, 12 heads of 64,
-// bf16: 62 us for 200 MB (3.2 TB/s), the two kernels 75 us for 300 MB; two
+// bf16: 66 us for 225 MB (3.4 TB/s), the two kernels 75 us for 300 MB; two
 // work-groups a CU by their LDS, whose loads and products overlap in part.
 constexpr int kShort = kBlock;
 
@@ -978,38 +1021,87 @@ __global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_b
   const int x1 = (lq + kTile - 1) / kTile;
   Pieces<T, NS> pq, pd, po;
   float stat = 0.f;
-  const auto bring = [&](int h, int x) {
+  // delta before the loop, so that waves may need P and dP for it; of fp32 from dO and o on their way through it
+  constexpr bool kDeltaFirst = sizeof(E) == 2;
+  const auto bring_tiles = [&](int h, int x) {
     const int64_t at = (int64_t)x * kTile * ldq + (int64_t)h * a.dim;
     pq.load(q + at, lq - x * kTile, lbq, a.dim);
     pd.load(d_o + at, lq - x * kTile, lbq, a.dim);
-    po.load(o + at, lq - x * kTile, lbq, a.dim);
-    if (threadIdx.x < kTile) {
-      const int i = x * kTile + threadIdx.x;
-      stat = i < lq ? lse[(int64_t)h * a.tq + i] : INFINITY;
+    if constexpr (!kDeltaFirst) po.load(o + at, lq - x * kTile, lbq, a.dim);
+  };
+  const auto bring_stat = [&](int h, int x) {
+    if (threadIdx.x < (kDeltaFirst ? 2 : 1) * kTile) {
+      const int i = x * kTile + (threadIdx.x & (kTile - 1));
+      const float* from = threadIdx.x < kTile ? lse : delta;
+      stat = i < lq ? from[(int64_t)h * a.tq + i] : threadIdx.x < kTile ? INFINITY : 0.f;
     }
   };
   const auto put = [&](int b) {
     pq.store(tiles + b * 2 * TS);
     pd.store(tiles + b * 2 * TS + TS);
+    if constexpr (!kDeltaFirst) {
 #pragma unroll
-    for (int n = 0; n < G::NL; ++n) {
-      float s = 0.f;
+      for (int n = 0; n < G::NL; ++n) {
+        float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < G::EPV; ++e) s += elem_to_f32<T>(pd.f[n][e]) * elem_to_f32<T>(po.f[n][e]);
-      dots[threadIdx.x + n * kThreads] = s;
+        for (int e = 0; e < G::EPV; ++e) s += elem_to_f32<T>(pd.f[n][e]) * elem_to_f32<T>(po.f[n][e]);
+        dots[threadIdx.x + n * kThreads] = s;
+      }
     }
-    if (threadIdx.x < kTile) stats[b][0][threadIdx.x] = stat;
+    if (threadIdx.x < (kDeltaFirst ? 2 : 1) * kTile) (&stats[b][0][0])[threadIdx.x] = stat;
   };
   int h = x1 > 0 ? 0 : group, x = 0, cur = 0;
   Own<T, NS> kf, vf;
   if (h < group) {
-    bring(0, 0);
-    Pieces<T, NS> pk[2];
+    {
+      Pieces<T, NS> pk[2];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) pk[y].load(k + (int64_t)y * kTile * ldk, lk - y * kTile, lbk, a.dim);
+      for (int y = 0; y < 2; ++y) pk[y].load(k + (int64_t)y * kTile * ldk, lk - y * kTile, lbk, a.dim);
+      bring_tiles(0, 0);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) pk[y].store(keys + y * TS);
+    }
+    if constexpr (kDeltaFirst) {
+      const int q0 = kOwn * wave, nq = min(lq - q0, kOwn), p0 = q0 + shift, p1 = p0 + nq - 1;
+      const bool few = nq > 0 && few_keys<E>(a, p0, p1, lk);
+      lds_barrier();
+#pragma unroll 1
+      for (int hh = 0; hh < (nq > 0 ? group : 0); ++hh) {
+        const int64_t at = (int64_t)q0 * ldq + (int64_t)hh * a.dim;
+        Own<T, NS> of, df;
+        of.load(o + at, nq, lbq, a.dim);
+        df.load(d_o + at, nq, lbq, a.dim);
+        float sum = 0.f;
+        if (few) {
+          of.load(q + at, nq, lbq, a.dim);
+          if (a.scale2 < 0.f) of.negate();
+          const float sub = c < nq ? lse[(int64_t)hh * a.tq + q0 + c] : INFINITY;
+#pragma unroll 1
+          for (int b = 0; b < blocks; ++b) {
+            if (none_seen(a, kOwn * b, kOwn, p0, p1, lk)) continue;
+            f32x16 s = rows_times_own<T, NS>(keys, b, of);
+            Own<T, NS> vr;
+            vr.load(v + (int64_t)kOwn * b * ldk, lk - kOwn * b, lbk, a.dim);
+            const f32x16 dp = vr.times(df);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, -sub)) * dp[i];
+            if (!all_seen(a, kOwn * b, kOwn, p0, p1, lk)) key_view(a, kOwn * b, p0 + c, lk).cut(s, 0.f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum += s[i];
+          }
+        } else {
+#pragma unroll
+          for (int f = 0; f < G::KF; ++f)
+#pragma unroll
+            for (int e = 0; e < G::EPV; ++e) sum += elem_to_f32<T>(of.f[f][e]) * elem_to_f32<T>(df.f[f][e]);
+        }
+        sum = sum_halves(sum);
+        if (c < nq && g == 0) delta[(int64_t)hh * a.tq + q0 + c] = sum;
+      }
+      __syncthreads();  // delta is there
+    }
+    bring_stat(0, 0);
     put(0);
-#pragma unroll
-    for (int y = 0; y < 2; ++y) pk[y].store(keys + y * TS);
   }
   kf.load(k + (int64_t)k0 * ldk, rows, lbk, a.dim);
   vf.load(v + (int64_t)k0 * ldk, rows, lbk, a.dim);
@@ -1021,8 +1113,11 @@ __global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_b
   while (h < group) {
     const int nx = x + 1 < x1 ? x + 1 : 0, nh = x + 1 < x1 ? h : h + 1;
     lds_barrier();
-    if (nh < group) bring(nh, nx);
-    if (threadIdx.x < kTile) {
+    if (nh < group) {
+      bring_tiles(nh, nx);
+      bring_stat(nh, nx);
+    }
+    if (!kDeltaFirst && threadIdx.x < kTile) {
       float s = 0.f;
 #pragma unroll
       for (int y = 0; y < G::CPR; ++y) s += dots[threadIdx.x * G::CPR + y];
@@ -1030,7 +1125,7 @@ __global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_b
       const int i = x * kTile + threadIdx.x;
       if (i < lq) delta[(int64_t)h * a.tq + i] = s;
     }
-    lds_barrier();
+    if (!kDeltaFirst) lds_barrier();
     const E *tq = tiles + cur * 2 * TS, *td = tq + TS;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {

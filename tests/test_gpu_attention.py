@@ -509,3 +509,28 @@ def test_short_sequences_with_bad_rows(which):
         assert torch.equal(x[n:], y[n:]), name
         far = torch.cat([torch.arange(1, 33), torch.arange(100, n)])  # rows that neither see row 60 nor meet one that does, the sink aside
         assert bool(torch.isfinite(x[far]).all()), name
+
+
+@pytest.mark.parametrize("lens,window,sinks,longest", [([1000], (1, 0), 0, 1000), ([1000], (1, 1), 1, 1000), ([700, 300], (3, 0), 0, 700),
+                                                       ([3] * 40 + [2] * 40, (-1, -1), 0, 3), ([2, 3, 4, 5, 6] * 20, (-1, 0), 0, None)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_of_few_keys_keep_their_precision(lens, window, sinks, longest, d):
+    """bf16: dq and dk carry two roundings, of dS and of themselves, each of at most half a step, 2^-8, and of 2^-8 / sqrt 3
+    in the root mean square; together 2^-8 sqrt(2 / 3) of the norm.  The rounding of o must not show in dS, which is a small
+    difference where a query sees few keys."""
+    ttc = _ttc()
+    q, k, v, do = _inputs(lens, lens, 4, 2, d, BF16, 11)
+    layer = ttc.WindowAttention(4, d, 2, window=window, sinks=sinks, dtype=BF16)
+    kw = dict(batch=len(lens), q_offsets=_offsets(lens), k_offsets=_offsets(lens), max_q=longest)
+    o, saved = layer.forward(q, k, v, **kw)
+    dq, dk, _ = layer.backward(q, k, v, o, do, saved, max_k=longest, **kw)
+    off, norm, at = [0.0, 0.0], [0.0, 0.0], 0
+    for n in lens:
+        cut = lambda t, w: t[at:at + n].view(n, w, d)  # noqa: E731
+        _, rq, rk, _ = _reference(cut(q, 4), cut(k, 2), cut(v, 2), cut(do, 4), _seen(n, n, *window, sinks, "cuda"), layer.desc.scale, 2.0 ** -8, 2)
+        for i, (got, (ref, _)) in enumerate(((cut(dq, 4), rq), (cut(dk, 2), rk))):
+            off[i] += float((got.double() - ref).square().sum())
+            norm[i] += float(ref.square().sum())
+        at += n
+    for x, y in zip(off, norm):
+        assert (x / y) ** 0.5 < 2.0 ** -8
