@@ -512,6 +512,11 @@ constexpr int key_groups() {
   return sizeof(typename Elem<T>::type) == 2 ? (NS <= 2 ? 3 : 2) : NS <= 2 ? 2 : 1;
 }
 
+// Bound by the vector units: for a tile of 64 keys a wave takes about 1000 cycles
+// of them (32 exponentials of 16 cycles, maxima, sums, masks, rounding) and 512
+// of matrix products, which overlap only across the waves of a SIMD.  2 x 8192,
+// 16 heads of 64, window 512 to both sides: 129 us, 520 TFLOP/s of what is
+// visible; prompts up to 2048, heads of 128: 240 us, 350 TFLOP/s.
 constexpr float kSlack = 8.f;  // P stays below 2^8 times its largest: far from overflow in fp32 and bf16
 
 template <typename T, int NS>
@@ -637,7 +642,8 @@ __device__ __forceinline__ bool few_keys(const AttnArgs& a, int p0, int p1, int 
   return sizeof(E) == 2 && min(keys_seen(a, p0, lk), keys_seen(a, p1, lk)) < kFewKeys;
 }
 
-// dq, and delta for k_attn_dkv
+// dq, and delta for k_attn_dkv: three products a tile, bound as k_attn_fwd is.
+// 2 x 8192: 150 us, 670 TFLOP/s of what is visible.
 template <typename T, int NS>
 __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(AttnArgs a) {
   typedef Geo<T, NS> G;
@@ -758,6 +764,12 @@ __global__ __launch_bounds__(kThreads, (key_groups<T, NS>())) void k_attn_dq(Att
 constexpr int kFar = 512;
 constexpr int kMaxFarSinks = kBlock;  // all sinks in the first block of keys
 
+// Four products a tile.  Bound by LDS: a 32 x 32 piece takes about 190 cycles of
+// its reads a wave (128 for the operands, 64 for lse and delta), 760 for the four
+// waves of a work-group, against 512 of a SIMD's products.  2 x 8192: 261 us, 510
+// TFLOP/s of what is visible; a third work-group on a CU costs 53 registers in
+// scratch and 413 us.
+//
 // work-groups that a CU holds: two where a wave's registers allow it
 template <typename T, int NS>
 constexpr int dkv_groups() {
@@ -940,7 +952,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_sinks(AttnArgs a) {
 // products instead of the seven of k_attn_dq and k_attn_dkv, and q, k, v and dO
 // are read once instead of twice.  dS goes through LDS, transposed, to the waves
 // that each sum a 32 x 32 piece of dq over all keys.  128 x 128, 12 heads of 64,
-// bf16: 66 us for 225 MB (3.4 TB/s), the two kernels 75 us for 300 MB; two
+// bf16: 64 us for 225 MB (3.5 TB/s), the two kernels 75 us for 300 MB; two
 // work-groups a CU by their LDS, whose loads and products overlap in part.
 constexpr int kShort = kBlock;
 
@@ -1053,6 +1065,14 @@ __global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_b
   int h = x1 > 0 ? 0 : group, x = 0, cur = 0;
   Own<T, NS> kf, vf;
   if (h < group) {
+    const int q0 = kOwn * wave, nq = min(lq - q0, kOwn), p0 = q0 + shift, p1 = p0 + nq - 1;
+    Own<T, NS> of, df;
+    const auto bring_own = [&](int hh) {
+      const int64_t at = (int64_t)q0 * ldq + (int64_t)hh * a.dim;
+      of.load(o + at, nq, lbq, a.dim);
+      df.load(d_o + at, nq, lbq, a.dim);
+    };
+    if constexpr (kDeltaFirst) bring_own(0);
     {
       Pieces<T, NS> pk[2];
 #pragma unroll
@@ -1062,18 +1082,13 @@ __global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_b
       for (int y = 0; y < 2; ++y) pk[y].store(keys + y * TS);
     }
     if constexpr (kDeltaFirst) {
-      const int q0 = kOwn * wave, nq = min(lq - q0, kOwn), p0 = q0 + shift, p1 = p0 + nq - 1;
       const bool few = nq > 0 && few_keys<E>(a, p0, p1, lk);
       lds_barrier();
 #pragma unroll 1
       for (int hh = 0; hh < (nq > 0 ? group : 0); ++hh) {
-        const int64_t at = (int64_t)q0 * ldq + (int64_t)hh * a.dim;
-        Own<T, NS> of, df;
-        of.load(o + at, nq, lbq, a.dim);
-        df.load(d_o + at, nq, lbq, a.dim);
         float sum = 0.f;
         if (few) {
-          of.load(q + at, nq, lbq, a.dim);
+          of.load(q + (int64_t)q0 * ldq + (int64_t)hh * a.dim, nq, lbq, a.dim);
           if (a.scale2 < 0.f) of.negate();
           const float sub = c < nq ? lse[(int64_t)hh * a.tq + q0 + c] : INFINITY;
 #pragma unroll 1
@@ -1097,6 +1112,7 @@ __global__ __launch_bounds__(kThreads, (ShortGeo<T, NS>::kGroups)) void k_attn_b
         }
         sum = sum_halves(sum);
         if (c < nq && g == 0) delta[(int64_t)hh * a.tq + q0 + c] = sum;
+        if (hh + 1 < group) bring_own(hh + 1);
       }
       __syncthreads();  // delta is there
     }
@@ -1266,7 +1282,8 @@ void launch(K kern, unsigned grid, size_t lds, hipStream_t s, const AttnArgs& a)
 
 // ---- one new token a sequence ----------------------------------------------------
 //
-// Bound by the cache's bytes.  A row of K or V is spread over LPR lanes, 16
+// Bound by the cache's bytes: 64 x 8192, 1023 keys back, 16 heads of 64, 255 MB in
+// 54 us, 4.7 TB/s (45 us where part of it lies in the caches).  A row of K or V is spread over LPR lanes, 16
 // bytes each, so a load of a wave brings 64 / LPR rows; each of these row
 // groups keeps a softmax of its own (maximum, sum, products) in registers, and
 // the groups, the waves and the splits of a long cache are joined at the end,

@@ -115,3 +115,19 @@ def test_ortho_errors_before_launch():
     for d in (dict(steps=0), dict(steps=33), dict(eps=0.0), dict(lr=float("nan")), dict(mu=float("inf")), dict(coeffs=(1.0, float("nan"), 0.0))):
         assert _code(lambda: call(d)) == 2, d
     ttc.ttc_ortho_step(ttc.make_ortho_desc(0.1), ttc.make_ortho_mats([]), None, 0, None, 0)
+
+
+def test_ortho_eps_below_the_normal_numbers_is_refused():
+    """1 / eps would pass the largest fp32 number."""
+    import ctypes
+    mats = ttc.make_ortho_mats([(240, 30, 16, 16, 16)])
+    pb, _ = ttc.ttc_ortho_workspace(mats)
+    host = ctypes.create_string_buffer(pb)
+    ttc.ttc_ortho_plan(mats, ctypes.addressof(host), pb)
+    assert _code(lambda: ttc.ttc_ortho_step(ttc.make_ortho_desc(0.1, eps=1e-40), mats, 16, pb, None, 0)) == 2
+
+
+def test_ortho_scratch_of_long_matrices():
+    """A matrix whose rows are cut into chunks needs scratch for their sums, whichever way it lies; a short one needs none."""
+    sizes = [ttc.ttc_ortho_workspace(ttc.make_ortho_mats([(r, c, 16, 16, 16)]))[1] for r, c in ((2048, 16), (2049, 16), (16, 2049), (1 << 20, 64))]
+    assert sizes[0] == 0 and 0 < sizes[1] == sizes[2] < sizes[3]
