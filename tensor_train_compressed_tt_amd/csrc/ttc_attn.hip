@@ -940,6 +940,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_sinks(AttnArgs a) {
     const int which = x >= n, y = x - which * n, j = y / a.dim, c = y - j * a.dim;
     const float* from = part + which * (int64_t)a.sinks * a.dim + y;
     float s = 0.f;
+#pragma unroll 8  // loads in flight; the sums keep their order
     for (int u = 0; u <= a.far; ++u) s += from[u * unit];
     static_cast<E*>(which ? a.dv : a.dk)[(sk.start + j) * ldk + (int64_t)head * a.dim + c] = Mma<T>::from_f32(s);
   }
