@@ -210,6 +210,8 @@ class WindowAttention:
         """o for one new token of each sequence: q (batch, heads * dim), the caches
         k and v (batch, capacity, kv_heads * dim), ``lens`` int32 rows in use (the
         new token's own among them); the window's right side has no meaning here."""
+        if q.dim() != 2 or k.dim() != 3:
+            raise ValueError("q must be (batch, heads * dim), k and v (batch, capacity, kv_heads * dim)")
         batch, capacity = int(q.shape[0]), int(k.shape[1])
         _need(q, "q", self.dtype, (batch, self.heads * self.dim))
         _need(k, "k", self.dtype, (batch, capacity, self.kv_heads * self.dim))

@@ -534,3 +534,13 @@ def test_gradients_of_few_keys_keep_their_precision(lens, window, sinks, longest
         at += n
     for x, y in zip(off, norm):
         assert (x / y) ** 0.5 < 2.0 ** -8
+
+
+def test_decode_refuses_caches_of_two_dimensions():
+    ttc = _ttc()
+    layer = ttc.WindowAttention(4, 64, 2, dtype=BF16)
+    z = lambda *s: torch.zeros(s, dtype=BF16, device="cuda")  # noqa: E731
+    lens = torch.ones(6, dtype=torch.int32, device="cuda")
+    for q, kv in ((z(6, 256), z(6, 128)), (z(6, 256), z(128)), (z(256), z(6, 9, 128))):
+        with pytest.raises(ValueError):
+            layer.decode(q, kv, kv, lens)
